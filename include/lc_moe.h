@@ -84,7 +84,8 @@ enum {
     LC_MOE_OP_ROUTE = 1,     /* lc_moe_route */
     LC_MOE_OP_PERMUTE = 2,   /* lc_moe_permute */
     LC_MOE_OP_STATUS = 3,    /* every other entry point: the status word only (256 bytes) */
-    LC_MOE_OP_FORWARD_FP8 = 4  /* lc_moe_forward_fp8 / _timed (0 unless d and I are multiples of 128) */
+    LC_MOE_OP_FORWARD_FP8 = 4, /* lc_moe_forward_fp8 / _timed (0 unless d and I are multiples of 128) */
+    LC_MOE_OP_FORWARD_W4 = 5   /* lc_moe_forward_w4 */
 };
 
 /* Stages of lc_moe_forward, in launch order (lc_moe_forward_timed records one event before
@@ -326,6 +327,104 @@ int lc_moe_forward_fp8_timed(const lc_moe_shape* s, const void* x, const void* w
                              const float* w2_scale, void* out, int32_t* idx, float* gate,
                              int32_t* counts, void* ws, size_t ws_bytes, void* stream,
                              void* const* events);
+
+/* ---- general gates and their gradient -------------------------------------------------------
+ * lc_moe_topk routes by a softmax over all experts with renormalised gates. The calls below take
+ * the scores, a first choice among groups of experts, the normalisation and a factor as options:
+ *   scores  s_i = softmax(z)_i over all E = N + Z experts, or 1 / (1 + e^-z_i)
+ *   keys    key_i = s_i + b_i (b steers the choice only; -inf switches an expert off)
+ *   groups  E / groups consecutive experts each; a group's score is the sum of its group_rank
+ *           largest keys (of its only key where it has one expert); the top_groups groups with the
+ *           largest scores stay, equal scores to the lower group
+ *   picks   the K largest keys of the groups that stay, in descending order, equal keys to the
+ *           lower expert
+ *   gates   g_r = scale * s_r, or with renorm scale * s_r / (sum of the K chosen s), 0 where that
+ *           sum is 0
+ * Picks are decided in 64 bits (keys closer than fp32 resolves are told apart); gates are fp32. A
+ * logit of -inf has score 0, and a row of them has all scores 0. A token with a NaN key (a NaN
+ * logit, +inf under softmax, a NaN bias) or a NaN group score (biases of both infinities) gets the
+ * picks 0..K-1, NaN gates and LC_MOE_DEV_NAN_KEY. K picks are always made: where fewer than K
+ * experts are switched on in the groups that stay, the rest are switched-off ones in index order.
+ */
+enum { LC_MOE_SCORE_SOFTMAX = 0, LC_MOE_SCORE_SIGMOID = 1 };
+
+/* Types of the logits (and of their gradient). */
+enum { LC_MOE_F32 = 0, LC_MOE_BF16 = 1 };
+
+/* Options of the general gates; NULL stands for {softmax, 1, 1, 1, 1, 1.0f}. */
+typedef struct lc_moe_gate_opts {
+    int32_t score;       /* LC_MOE_SCORE_* */
+    int32_t groups;      /* 1..32, divides N + Z (else LC_MOE_ERR_UNSUPPORTED_SHAPE) */
+    int32_t top_groups;  /* 1..groups; top_groups * (N + Z) / groups >= K (else UNSUPPORTED_SHAPE) */
+    int32_t group_rank;  /* 1 or 2 */
+    int32_t renorm;      /* 0 or 1 */
+    float scale;         /* finite */
+} lc_moe_gate_opts;
+
+/* logits [T, E] fp32 or bf16 (4- or 2-byte aligned) -> idx [T, K] int32, gate [T, K] fp32; bias [E]
+ * fp32 or NULL (none); counts [E] int32 optional, ADDED TO. ws: status only. */
+int lc_moe_gate(const lc_moe_shape* s, const lc_moe_gate_opts* o, const void* logits, int32_t logits_type,
+                const float* bias, int32_t* idx, float* gate, int32_t* counts, void* ws, size_t ws_bytes,
+                void* stream);
+
+/* Gradient of the gates for the logits, the picks held fixed: dlogits [T, E] (the logits' type; not
+ * the logits' own buffer) from logits, idx [T, K] and dgate [T, K] fp32. Of the options score,
+ * renorm and scale count. An entry of idx outside [0, E) sets LC_MOE_DEV_IDX_RANGE and counts as
+ * no pick; an expert picked twice gets the sum. The bias has no gradient. ws: status only. */
+int lc_moe_gate_backward(const lc_moe_shape* s, const lc_moe_gate_opts* o, const void* logits,
+                         int32_t logits_type, const int32_t* idx, const float* dgate, void* dlogits, void* ws,
+                         size_t ws_bytes, void* stream);
+
+/* Gradient of lc_moe_combine: from dout [T, d] bf16 and the forward's x, y [y_rows, d], gate and
+ * pair_row,
+ *   dgate [T, K] fp32 = <dout_t, y[pair_row[t,r]] or x_t>
+ *   dy [y_rows, d] bf16: row pair_row[t,r] = gate[t,r] dout_t; rows in no pick are not written
+ *   dx [T, d] bf16 = (sum of the gates of t's zero picks) dout_t: x's gradient through the zero
+ *   experts alone
+ * with fp32 products and sums. pair_row as lc_moe_permute makes it: a row is in one pick at most.
+ * An entry >= y_rows sets LC_MOE_DEV_IDX_RANGE; its dgate is 0. dout, x, y are not written and must
+ * not overlap dy and dx. ws: status only. */
+int lc_moe_combine_backward(const lc_moe_shape* s, const void* dout, const void* x, const void* y, int64_t y_rows,
+                            const float* gate, const int32_t* pair_row, void* dy, float* dgate, void* dx, void* ws,
+                            size_t ws_bytes, void* stream);
+
+/* ---- 4-bit experts --------------------------------------------------------------------------
+ * w[r, c] = (code[r, c] - 8) * scale[r, c / group], codes 0..15, one bf16 scale per row and group of
+ * 32, 64 or 128 columns (d and I multiples of the group, else LC_MOE_ERR_UNSUPPORTED_SHAPE).
+ * Activations stay bf16. The products run as a stream of the codes, for batches that give an expert
+ * few rows (decode); any number of rows is computed.
+ *
+ * Layout of a matrix [rows, cols] (rows % 16 == 0, cols % 64 == 0):
+ *   codes [rows, cols / 2] bytes in tiles of 16 rows x 64 columns, 512 bytes each, tile (r/16, c/64)
+ *   at index (r/16) * (cols/64) + c/64. Within its tile, element (r, c) is in the little-endian
+ *   32-bit word at byte 16 * (4 * (r%8) + (c%32)/8) + 4 * (2 * ((c%64)/32) + (r%16)/8), in bits
+ *   4p .. 4p+3 with p = (c%8)/2 + 4 * (c%2).
+ *   scale [rows / 16, cols / group, 16] bf16: row r at [r/16, :, 2 * (r%8) + (r%16)/8].
+ */
+
+/* 4-bit quantisation of a bf16 matrix src [rows, cols] into that layout: scale = bf16(amax / 7) of
+ * each group (1 where that is 0), code = 8 + w / scale rounded to nearest even, within 1..15, with
+ * fp32 divisions. Finite weights. Several matrices of the same shape one after another are one
+ * matrix: w13 is [N * 2I, d], w2 is [N * d, I]. rows % 16 == 0, cols % 64 == 0, cols % group == 0
+ * (else LC_MOE_ERR_INVALID_ARG). */
+int lc_moe_quantize_w4(const void* src, int64_t rows, int32_t cols, int32_t group, void* codes, void* scale,
+                       void* stream);
+
+/* lc_moe_expert_ffn with 4-bit experts: w13q [N, 2I, d/2] with w13_scale [N, 2I/16, d/group, 16],
+ * w2q [N, d, I/2] with w2_scale [N, d/16, I/group, 16]. h and y as there (bf16 at both); rows
+ * >= offsets[N] are not written. An expert whose rows are not within [0, T*K] sets
+ * LC_MOE_DEV_IDX_RANGE and is skipped. ws: status only. */
+int lc_moe_expert_ffn_w4(const lc_moe_shape* s, const void* x_perm, const int32_t* offsets, const void* w13q,
+                         const void* w13_scale, const void* w2q, const void* w2_scale, int32_t group, void* h,
+                         void* y, void* ws, size_t ws_bytes, void* stream);
+
+/* lc_moe_forward with 4-bit experts and any gate: o = NULL routes exactly as lc_moe_forward does
+ * (the bits of lc_moe_topk), otherwise as lc_moe_gate. bias [E] fp32, NULL allowed when o is given.
+ * ws: lc_moe_workspace_bytes(s, LC_MOE_OP_FORWARD_W4) bytes. */
+int lc_moe_forward_w4(const lc_moe_shape* s, const lc_moe_gate_opts* o, const void* x, const void* wr,
+                      const float* bias, const void* w13q, const void* w13_scale, const void* w2q,
+                      const void* w2_scale, int32_t group, void* out, int32_t* idx, float* gate, int32_t* counts,
+                      void* ws, size_t ws_bytes, void* stream);
 
 #ifdef __cplusplus
 }

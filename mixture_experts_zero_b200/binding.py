@@ -7,6 +7,7 @@ The library is loaded on first use. If it has not been built, or the device is n
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes
 import pathlib
 import threading
@@ -21,7 +22,9 @@ OK = 0
 ERR_INVALID_ARG, ERR_UNSUPPORTED_SHAPE, ERR_WORKSPACE_TOO_SMALL, ERR_NOT_SM100 = 1, 2, 3, 4
 ERR_CUDA, ERR_DEVICE_STATUS, ERR_TIMEOUT, ERR_MISALIGNED = 5, 6, 7, 8
 DEV_IDX_RANGE, DEV_NAN_KEY, DEV_WAIT_TIMEOUT, DEV_DUP_PICK = 0x1, 0x2, 0x4, 0x8
-OP_FORWARD, OP_ROUTE, OP_PERMUTE, OP_STATUS, OP_FORWARD_FP8 = 0, 1, 2, 3, 4
+OP_FORWARD, OP_ROUTE, OP_PERMUTE, OP_STATUS, OP_FORWARD_FP8, OP_FORWARD_W4 = 0, 1, 2, 3, 4, 5
+SCORES = {"softmax": 0, "sigmoid": 1}
+LOGITS_TYPES = {torch.float32: 0, torch.bfloat16: 1}
 NUM_STAGES = 7
 STAGE_NAMES = ("router_gemm", "topk", "permute", "gather", "gemm1_swiglu", "gemm2_down", "combine")
 
@@ -32,12 +35,19 @@ EXPORTED = (
     "lc_moe_permute", "lc_moe_expert_ffn", "lc_moe_combine", "lc_moe_permute_noalloc",
     "lc_moe_quantize_e4m3", "lc_moe_forward_fp8", "lc_moe_forward_fp8_timed",
     "lc_moe_check_wait_timeout", "lc_moe_ep_regroup_plan", "lc_moe_copy_rows", "lc_moe_set_clock_probe",
+    "lc_moe_gate", "lc_moe_gate_backward", "lc_moe_combine_backward", "lc_moe_quantize_w4",
+    "lc_moe_expert_ffn_w4", "lc_moe_forward_w4",
 )
 
 
 class Shape(ctypes.Structure):
     _fields_ = [("T", ctypes.c_int32), ("d", ctypes.c_int32), ("N", ctypes.c_int32),
                 ("Z", ctypes.c_int32), ("K", ctypes.c_int32), ("I", ctypes.c_int32)]
+
+
+class GateOpts(ctypes.Structure):
+    _fields_ = [("score", ctypes.c_int32), ("groups", ctypes.c_int32), ("top_groups", ctypes.c_int32),
+                ("group_rank", ctypes.c_int32), ("renorm", ctypes.c_int32), ("scale", ctypes.c_float)]
 
 
 class LcMoeError(RuntimeError):
@@ -95,6 +105,13 @@ def _configure(L: ctypes.CDLL) -> ctypes.CDLL:
     L.lc_moe_check_wait_timeout.argtypes = [P, SZ, P]
     L.lc_moe_ep_regroup_plan.argtypes = [P, I32, I32, P, I64, P, P, SZ, P]
     L.lc_moe_copy_rows.argtypes = [P, P, P, I64, I32, I32, P, SZ, P]
+    GP = ctypes.POINTER(GateOpts)
+    L.lc_moe_gate.argtypes = [SP, GP, P, I32, P, P, P, P, P, SZ, P]
+    L.lc_moe_gate_backward.argtypes = [SP, GP, P, I32, P, P, P, P, SZ, P]
+    L.lc_moe_combine_backward.argtypes = [SP, P, P, P, I64, P, P, P, P, P, P, SZ, P]
+    L.lc_moe_quantize_w4.argtypes = [P, I64, I32, I32, P, P, P]
+    L.lc_moe_expert_ffn_w4.argtypes = [SP, P, P, P, P, P, P, I32, P, P, P, SZ, P]
+    L.lc_moe_forward_w4.argtypes = [SP, GP, P, P, P, P, P, P, P, I32, P, P, P, P, P, SZ, P]
     return L
 
 
@@ -505,4 +522,228 @@ def lc_moe_copy_rows(src, index, scatter: bool = False, out=None, ws=None, strea
         ws = _status_ws(src.device)
     _check(_lib().lc_moe_copy_rows(_ptr(src), _ptr(out), _ptr(index), n, row_bytes, 1 if scatter else 0,
                                    _ptr(ws), ws.numel(), _stream(stream)), "lc_moe_copy_rows")
+    return out
+
+
+# ------------------------------------------------- general gates, gradients, 4-bit experts --
+
+def _one_device(**tensors):
+    """Every given tensor is a contiguous CUDA tensor of the current device (the library launches
+    there)."""
+    cur = torch.cuda.current_device() if torch.cuda.is_available() else None
+    for name, t in tensors.items():
+        if t is None:
+            continue
+        if not t.is_cuda or not t.is_contiguous():
+            raise ValueError(f"{name}: expected a contiguous CUDA tensor")
+        if t.device.index != cur:
+            raise ValueError(f"{name}: on {t.device}, but the current device is cuda:{cur}")
+
+
+def _alloc_on(stream):
+    """Buffers that a call makes itself belong to the stream it runs on."""
+    return contextlib.nullcontext() if stream is None else torch.cuda.stream(stream)
+
+
+def _dims_of(t, n, name):
+    if t.dim() != n:
+        raise ValueError(f"{name}: expected {n} dimensions, got {t.dim()}")
+    return tuple(t.shape)
+
+
+def _gate_opts(score, groups, top_groups, group_rank, renorm, scale) -> GateOpts:
+    if score not in SCORES:
+        raise ValueError(f"score: expected one of {sorted(SCORES)}, got {score!r}")
+    return GateOpts(SCORES[score], groups, top_groups, group_rank, int(bool(renorm)), scale)
+
+
+def lc_moe_gate(logits, bias, K: int, N: int, score: str = "softmax", groups: int = 1, top_groups: int = 1,
+                group_rank: int = 1, renorm: bool = True, scale: float = 1.0, idx=None, gate=None, counts=None,
+                ws=None, stream=None):
+    """General gates from logits [T, E] (fp32 or bf16): ``score`` "softmax" or "sigmoid", ``bias``
+    fp32 [E] or None, the ``top_groups`` best of ``groups`` groups of experts (by the sum of their
+    ``group_rank`` largest keys), gates renormalised or not, times ``scale``. Returns (idx, gate)."""
+    T, E = _dims_of(logits, 2, "logits")
+    if logits.dtype not in LOGITS_TYPES:
+        raise TypeError(f"logits: expected float32 or bfloat16, got {logits.dtype}")
+    _one_device(logits=logits, bias=bias, idx=idx, gate=gate, counts=counts, ws=ws)
+    o = _gate_opts(score, groups, top_groups, group_rank, renorm, scale)
+    if bias is not None:
+        _need(bias, torch.float32, (E,), "bias")
+    with _alloc_on(stream):
+        if idx is None:
+            idx = torch.empty(T, K, dtype=torch.int32, device=logits.device)
+        if gate is None:
+            gate = torch.empty(T, K, dtype=torch.float32, device=logits.device)
+        if ws is None:
+            ws = _status_ws(logits.device)
+    _need(idx, torch.int32, (T, K), "idx")
+    _need(gate, torch.float32, (T, K), "gate")
+    if counts is not None:
+        _need(counts, torch.int32, (E,), "counts")
+    s = Shape(T, 64, N, E - N, K, 64)
+    _check(_lib().lc_moe_gate(ctypes.byref(s), ctypes.byref(o), _ptr(logits), LOGITS_TYPES[logits.dtype], _ptr(bias),
+                              _ptr(idx), _ptr(gate), _ptr(counts), _ptr(ws), ws.numel(), _stream(stream)),
+           "lc_moe_gate")
+    return idx, gate
+
+
+def lc_moe_gate_backward(logits, idx, dgate, score: str = "softmax", renorm: bool = True, scale: float = 1.0,
+                         dlogits=None, ws=None, stream=None):
+    """Gradient of lc_moe_gate's gates for the logits, the picks ``idx`` held fixed."""
+    T, E = _dims_of(logits, 2, "logits")
+    K = _dims_of(idx, 2, "idx")[1]
+    if logits.dtype not in LOGITS_TYPES:
+        raise TypeError(f"logits: expected float32 or bfloat16, got {logits.dtype}")
+    _one_device(logits=logits, idx=idx, dgate=dgate, dlogits=dlogits, ws=ws)
+    o = _gate_opts(score, 1, 1, 1, renorm, scale)
+    _need(idx, torch.int32, (T, K), "idx")
+    _need(dgate, torch.float32, (T, K), "dgate")
+    with _alloc_on(stream):
+        if dlogits is None:
+            dlogits = torch.empty_like(logits)
+        if ws is None:
+            ws = _status_ws(logits.device)
+    _need(dlogits, logits.dtype, (T, E), "dlogits")
+    s = Shape(T, 64, E, 0, K, 64)
+    _check(_lib().lc_moe_gate_backward(ctypes.byref(s), ctypes.byref(o), _ptr(logits), LOGITS_TYPES[logits.dtype],
+                                       _ptr(idx), _ptr(dgate), _ptr(dlogits), _ptr(ws), ws.numel(), _stream(stream)),
+           "lc_moe_gate_backward")
+    return dlogits
+
+
+def lc_moe_combine_backward(dout, x, y, gate, pair_row, dy=None, dgate=None, dx=None, ws=None, stream=None):
+    """Gradient of lc_moe_combine. Returns (dy, dgate, dx): dy [rows, d] for the experts' rows (rows
+    in no pick are not written; a new dy has zeros there), dgate [T, K] fp32, and dx [T, d], x's
+    gradient through the zero experts alone."""
+    T, d = _dims_of(dout, 2, "dout")
+    K = _dims_of(gate, 2, "gate")[1]
+    rows = _dims_of(y, 2, "y")[0]
+    _one_device(dout=dout, x=x, y=y, gate=gate, pair_row=pair_row, dy=dy, dgate=dgate, dx=dx, ws=ws)
+    _need(dout, torch.bfloat16, (T, d), "dout")
+    _need(x, torch.bfloat16, (T, d), "x")
+    _need(y, torch.bfloat16, (rows, d), "y")
+    _need(gate, torch.float32, (T, K), "gate")
+    _need(pair_row, torch.int32, (T, K), "pair_row")
+    with _alloc_on(stream):
+        if dy is None:
+            dy = torch.zeros_like(y)
+        if dgate is None:
+            dgate = torch.empty(T, K, dtype=torch.float32, device=dout.device)
+        if dx is None:
+            dx = torch.empty_like(dout)
+        if ws is None:
+            ws = _status_ws(dout.device)
+    _need(dy, torch.bfloat16, (rows, d), "dy")
+    _need(dgate, torch.float32, (T, K), "dgate")
+    _need(dx, torch.bfloat16, (T, d), "dx")
+    s = Shape(T, d, 1, K, K, 64)
+    _check(_lib().lc_moe_combine_backward(ctypes.byref(s), _ptr(dout), _ptr(x), _ptr(y), rows, _ptr(gate),
+                                          _ptr(pair_row), _ptr(dy), _ptr(dgate), _ptr(dx), _ptr(ws), ws.numel(),
+                                          _stream(stream)), "lc_moe_combine_backward")
+    return dy, dgate, dx
+
+
+def lc_moe_quantize_w4(src, group: int = 64, codes=None, scale=None, stream=None):
+    """4-bit quantisation of bf16 matrices [..., rows, cols] in the library's tiled layout. Returns
+    (codes uint8 [..., rows, cols / 2], scale bf16 [..., rows / 16, cols / group, 16])."""
+    if src.dim() < 2:
+        raise ValueError("src: expected [..., rows, cols]")
+    _one_device(src=src, codes=codes, scale=scale)
+    *lead, rows, cols = src.shape
+    _need(src, torch.bfloat16, tuple(src.shape), "src")
+    if group not in (32, 64, 128) or rows % 16 or cols % 64 or cols % group:
+        raise ValueError(f"src: rows % 16, cols % 64 and cols % group (32, 64 or 128) must be 0, got {rows} x {cols}, "
+                         f"group {group}")
+    with _alloc_on(stream):
+        if codes is None:
+            codes = torch.empty(*lead, rows, cols // 2, dtype=torch.uint8, device=src.device)
+        if scale is None:
+            scale = torch.empty(*lead, rows // 16, cols // group, 16, dtype=torch.bfloat16, device=src.device)
+    _need(codes, torch.uint8, (*lead, rows, cols // 2), "codes")
+    _need(scale, torch.bfloat16, (*lead, rows // 16, cols // group, 16), "scale")
+    if src.numel():
+        _check(_lib().lc_moe_quantize_w4(_ptr(src), src.numel() // cols, cols, group, _ptr(codes), _ptr(scale),
+                                         _stream(stream)), "lc_moe_quantize_w4")
+    return codes, scale
+
+
+def _w4_dims(w13q, w13_scale, w2q, w2_scale):
+    N, two_i, half_d = _dims_of(w13q, 3, "w13q")
+    I, d = two_i // 2, 2 * half_d
+    groups = _dims_of(w13_scale, 4, "w13_scale")[2]
+    if groups < 1 or d % groups:
+        raise ValueError(f"w13_scale: {groups} groups do not divide d = {d}")
+    group = d // groups
+    if group not in (32, 64, 128) or d % group or I % group:
+        raise ValueError(f"w13_scale: groups of {group} columns, expected 32, 64 or 128 that divide d = {d} and I = {I}")
+    _need(w13q, torch.uint8, (N, 2 * I, d // 2), "w13q")
+    _need(w13_scale, torch.bfloat16, (N, 2 * I // 16, d // group, 16), "w13_scale")
+    _need(w2q, torch.uint8, (N, d, I // 2), "w2q")
+    _need(w2_scale, torch.bfloat16, (N, d // 16, I // group, 16), "w2_scale")
+    return N, d, I, group
+
+
+def lc_moe_expert_ffn_w4(x_perm, offsets, w13q, w13_scale, w2q, w2_scale, T: int, K: int, h=None, y=None, ws=None,
+                         stream=None):
+    """lc_moe_expert_ffn with 4-bit experts (codes and scales as lc_moe_quantize_w4 makes them).
+    Returns (h, y); rows behind offsets[N] are not written."""
+    _one_device(x_perm=x_perm, offsets=offsets, w13q=w13q, w13_scale=w13_scale, w2q=w2q, w2_scale=w2_scale, h=h, y=y,
+                ws=ws)
+    N, d, I, group = _w4_dims(w13q, w13_scale, w2q, w2_scale)
+    rows = T * K
+    _need(x_perm, torch.bfloat16, (rows, d), "x_perm")
+    _need(offsets, torch.int32, (N + 1,), "offsets")
+    with _alloc_on(stream):
+        if h is None:
+            h = torch.empty(rows, I, dtype=torch.bfloat16, device=x_perm.device)
+        if y is None:
+            y = torch.empty(rows, d, dtype=torch.bfloat16, device=x_perm.device)
+        if ws is None:
+            ws = _status_ws(x_perm.device)
+    _need(h, torch.bfloat16, (rows, I), "h")
+    _need(y, torch.bfloat16, (rows, d), "y")
+    s = Shape(T, d, N, max(0, K - N), K, I)
+    _check(_lib().lc_moe_expert_ffn_w4(ctypes.byref(s), _ptr(x_perm), _ptr(offsets), _ptr(w13q), _ptr(w13_scale),
+                                       _ptr(w2q), _ptr(w2_scale), group, _ptr(h), _ptr(y), _ptr(ws), ws.numel(),
+                                       _stream(stream)), "lc_moe_expert_ffn_w4")
+    return h, y
+
+
+def lc_moe_forward_w4(x, wr, bias, w13q, w13_scale, w2q, w2_scale, K: int, opts: dict | None = None, out=None,
+                      idx=None, gate=None, counts=None, ws=None, stream=None):
+    """MoE(x) with 4-bit experts (lc_moe_quantize_w4). ``opts``: the options of lc_moe_gate (score,
+    groups, top_groups, group_rank, renorm, scale), or None to route exactly as lc_moe_forward does.
+    Returns ``out`` [T, d] bf16."""
+    T, d = _dims_of(x, 2, "x")
+    E = _dims_of(wr, 2, "wr")[0]
+    _one_device(x=x, wr=wr, bias=bias, w13q=w13q, w13_scale=w13_scale, w2q=w2q, w2_scale=w2_scale, out=out, idx=idx,
+                gate=gate, counts=counts, ws=ws)
+    N, dw, I, group = _w4_dims(w13q, w13_scale, w2q, w2_scale)
+    o = None
+    if opts is not None:
+        o = _gate_opts(**{**dict(score="softmax", groups=1, top_groups=1, group_rank=1, renorm=True, scale=1.0), **opts})
+    _need(x, torch.bfloat16, (T, dw), "x")
+    _need(wr, torch.bfloat16, (E, dw), "wr")
+    if bias is not None:
+        _need(bias, torch.float32, (E,), "bias")
+    elif opts is None:
+        raise ValueError("bias: required without opts")
+    s = Shape(T, d, N, E - N, K, I)
+    with _alloc_on(stream):
+        if out is None:
+            out = torch.empty(T, d, dtype=torch.bfloat16, device=x.device)
+        if ws is None:
+            ws = new_workspace(s, OP_FORWARD_W4, x.device)
+    _need(out, torch.bfloat16, (T, d), "out")
+    if idx is not None:
+        _need(idx, torch.int32, (T, K), "idx")
+    if gate is not None:
+        _need(gate, torch.float32, (T, K), "gate")
+    if counts is not None:
+        _need(counts, torch.int32, (E,), "counts")
+    _check(_lib().lc_moe_forward_w4(ctypes.byref(s), None if o is None else ctypes.byref(o), _ptr(x), _ptr(wr),
+                                    _ptr(bias), _ptr(w13q), _ptr(w13_scale), _ptr(w2q), _ptr(w2_scale), group,
+                                    _ptr(out), _ptr(idx), _ptr(gate), _ptr(counts), _ptr(ws), ws.numel(),
+                                    _stream(stream)), "lc_moe_forward_w4")
     return out

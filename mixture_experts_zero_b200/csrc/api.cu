@@ -110,19 +110,46 @@ int record(void* const* events, int i, cudaStream_t st) {
     return cuda_status(cudaEventRecord(static_cast<cudaEvent_t>(events[i]), st));
 }
 
-int forward_impl(const lc_moe_shape* s, const void* x, const void* wr, const float* bias,
-                 const void* w13, const float* w13_scale, const void* w2, const float* w2_scale,
+constexpr lc_moe_gate_opts kDefaultGate{LC_MOE_SCORE_SOFTMAX, 1, 1, 1, 1, 1.0f};
+
+// Options of the general gates for a checked shape.
+int check_gate(const lc_moe_shape* s, const lc_moe_gate_opts* o) {
+    if (o->score != LC_MOE_SCORE_SOFTMAX && o->score != LC_MOE_SCORE_SIGMOID) return LC_MOE_ERR_INVALID_ARG;
+    if (o->groups < 1 || o->top_groups < 1 || o->top_groups > o->groups || (o->group_rank != 1 && o->group_rank != 2) ||
+        (o->renorm != 0 && o->renorm != 1) || !(o->scale - o->scale == 0.0f))
+        return LC_MOE_ERR_INVALID_ARG;
+    const int E = s->N + s->Z;
+    if (o->groups > 32 || E % o->groups || static_cast<int64_t>(o->top_groups) * (E / o->groups) < s->K)
+        return LC_MOE_ERR_UNSUPPORTED_SHAPE;
+    return LC_MOE_OK;
+}
+
+// Group of the 4-bit weights for a checked shape (0: not 4-bit weights).
+int check_group(const lc_moe_shape* s, int32_t group) {
+    if (group != 32 && group != 64 && group != 128) return LC_MOE_ERR_INVALID_ARG;
+    return s->d % group || s->I % group ? LC_MOE_ERR_UNSUPPORTED_SHAPE : LC_MOE_OK;
+}
+
+// What the experts' weights are: bf16, E4M3 codes with fp32 row scales, or 4-bit codes with bf16
+// scales per group of columns.
+enum Experts { EXPERTS_BF16, EXPERTS_E4M3, EXPERTS_W4 };
+
+int forward_impl(const lc_moe_shape* s, Experts kind, const void* x, const void* wr, const float* bias,
+                 const void* w13, const void* w13_scale, const void* w2, const void* w2_scale,
                  void* out, int32_t* idx, float* gate, int32_t* counts, void* ws, size_t ws_bytes,
-                 void* stream, void* const* events) {
-    // w13_scale != NULL selects the E4M3 experts (w13 and w2 then hold E4M3 codes)
-    const bool f8 = w13_scale != nullptr;
+                 void* stream, void* const* events, int32_t group = 0, const lc_moe_gate_opts* o = nullptr) {
+    const bool f8 = kind == EXPERTS_E4M3;
     LC_TRY(check_shape(s));
     if (f8 && (s->d % 128 || s->I % 128)) return LC_MOE_ERR_UNSUPPORTED_SHAPE;
-    if (!x || !wr || !bias || !w13 || !w2 || !out || !ws || (f8 && !w2_scale)) return LC_MOE_ERR_INVALID_ARG;
+    if (kind == EXPERTS_W4) LC_TRY(check_group(s, group));
+    if (o) LC_TRY(check_gate(s, o));
+    if (kind == EXPERTS_W4 && s->T == 0) return LC_MOE_OK;  // empty tensors may be null pointers
+    if (!x || !wr || (!bias && !o) || !w13 || !w2 || !out || !ws || (kind != EXPERTS_BF16 && (!w13_scale || !w2_scale)))
+        return LC_MOE_ERR_INVALID_ARG;
     const FwdLayout L = fwd_layout(s, f8);
     if (ws_bytes < L.total) return LC_MOE_ERR_WORKSPACE_TOO_SMALL;
-    for (const void* p : {x, wr, static_cast<const void*>(bias), w13, static_cast<const void*>(w13_scale), w2,
-                          static_cast<const void*>(w2_scale), static_cast<const void*>(out),
+    for (const void* p : {x, wr, static_cast<const void*>(bias), w13, w13_scale, w2,
+                          w2_scale, static_cast<const void*>(out),
                           static_cast<const void*>(idx), static_cast<const void*>(gate),
                           static_cast<const void*>(counts), static_cast<const void*>(ws)})
         if (p && !aligned16(p)) return LC_MOE_ERR_MISALIGNED;
@@ -145,7 +172,8 @@ int forward_impl(const lc_moe_shape* s, const void* x, const void* wr, const flo
     LC_TRY(record(events, LC_MOE_STAGE_ROUTER_GEMM, st));
     LC_CUDA(launch_router_gemm(x, wr, logits, s->T, s->d, E, status, st));
     LC_TRY(record(events, LC_MOE_STAGE_TOPK, st));
-    LC_CUDA(launch_topk(logits, bias, s->T, E, s->K, idx_w, gate_w, counts, status, st));
+    if (o) LC_CUDA(launch_gate(logits, 0, bias, s->T, E, s->K, *o, idx_w, gate_w, counts, status, st));
+    else LC_CUDA(launch_topk(logits, bias, s->T, E, s->K, idx_w, gate_w, counts, status, st));
     LC_TRY(record(events, LC_MOE_STAGE_PERMUTE, st));
     LC_CUDA(launch_permute(idx_w, s->T, s->K, s->N, E, offsets, row_token, pair_row, scratch, status, st));
     LC_TRY(record(events, LC_MOE_STAGE_GATHER, st));
@@ -157,12 +185,15 @@ int forward_impl(const lc_moe_shape* s, const void* x, const void* wr, const flo
         LC_CUDA(launch_quantize_rows_e4m3(x, s->T, s->d, xq, sx, st));
         LC_CUDA(launch_gather_e4m3(xq, sx, s->T, s->d, s->K, pair_row, x_perm, s_row, status, st));
         LC_TRY(record(events, LC_MOE_STAGE_GEMM1, st));
-        LC_CUDA(launch_grouped_swiglu_e4m3(x_perm, s_row, L.rows_cap, offsets, s->N, w13, w13_scale, s->d,
-                                           s->I, h, status, st));
+        LC_CUDA(launch_grouped_swiglu_e4m3(x_perm, s_row, L.rows_cap, offsets, s->N, w13,
+                                           static_cast<const float*>(w13_scale), s->d, s->I, h, status, st));
     } else {
         LC_CUDA(launch_gather(x, s->T, s->d, s->K, pair_row, x_perm, status, st));
         LC_TRY(record(events, LC_MOE_STAGE_GEMM1, st));
-        LC_CUDA(launch_grouped_swiglu(x_perm, L.rows_cap, offsets, s->N, w13, s->d, s->I, h, status, st));
+        if (kind == EXPERTS_W4)
+            LC_CUDA(launch_swiglu_w4(x_perm, L.rows_cap, offsets, s->N, w13, w13_scale, group, s->d, s->I, h, status,
+                                     st));
+        else LC_CUDA(launch_grouped_swiglu(x_perm, L.rows_cap, offsets, s->N, w13, s->d, s->I, h, status, st));
     }
     LC_TRY(record(events, LC_MOE_STAGE_GEMM2, st));
     if (f8) {
@@ -170,8 +201,10 @@ int forward_impl(const lc_moe_shape* s, const void* x, const void* wr, const flo
         void* hq = at<void>(ws, L.hq);
         float* s_h = at<float>(ws, L.s_h);
         LC_CUDA(launch_quantize_rows_e4m3(h, L.rows_cap, s->I, hq, s_h, st, offsets + s->N));
-        LC_CUDA(launch_grouped_down_e4m3(hq, s_h, L.rows_cap, offsets, s->N, w2, w2_scale, s->d, s->I, y,
-                                         status, st));
+        LC_CUDA(launch_grouped_down_e4m3(hq, s_h, L.rows_cap, offsets, s->N, w2,
+                                         static_cast<const float*>(w2_scale), s->d, s->I, y, status, st));
+    } else if (kind == EXPERTS_W4) {
+        LC_CUDA(launch_down_w4(h, L.rows_cap, offsets, s->N, w2, w2_scale, group, s->d, s->I, y, status, st));
     } else {
         LC_CUDA(launch_grouped_down(h, L.rows_cap, offsets, s->N, w2, s->d, s->I, y, status, st));
     }
@@ -235,7 +268,8 @@ const char* lc_moe_strerror(int code) {
 size_t lc_moe_workspace_bytes(const lc_moe_shape* s, int op) {
     if (check_shape(s) != LC_MOE_OK) return 0;
     switch (op) {
-        case LC_MOE_OP_FORWARD: return fwd_layout(s).total;
+        case LC_MOE_OP_FORWARD:
+        case LC_MOE_OP_FORWARD_W4: return fwd_layout(s).total;
         case LC_MOE_OP_FORWARD_FP8: return (s->d % 128 || s->I % 128) ? 0 : fwd_layout(s, true).total;
         case LC_MOE_OP_ROUTE: return route_ws_bytes(s);
         case LC_MOE_OP_PERMUTE: return permute_ws_bytes(s);
@@ -265,7 +299,7 @@ int lc_moe_check_wait_timeout(void* ws, size_t ws_bytes, void* stream) {
 int lc_moe_forward(const lc_moe_shape* s, const void* x, const void* wr, const float* bias,
                    const void* w13, const void* w2, void* out, int32_t* idx, float* gate,
                    int32_t* counts, void* ws, size_t ws_bytes, void* stream) {
-    return forward_impl(s, x, wr, bias, w13, nullptr, w2, nullptr, out, idx, gate, counts, ws, ws_bytes, stream,
+    return forward_impl(s, EXPERTS_BF16, x, wr, bias, w13, nullptr, w2, nullptr, out, idx, gate, counts, ws, ws_bytes, stream,
                         nullptr);
 }
 
@@ -276,7 +310,7 @@ int lc_moe_forward_timed(const lc_moe_shape* s, const void* x, const void* wr, c
     if (!events) return LC_MOE_ERR_INVALID_ARG;
     for (int i = 0; i <= LC_MOE_NUM_STAGES; ++i)
         if (!events[i]) return LC_MOE_ERR_INVALID_ARG;
-    return forward_impl(s, x, wr, bias, w13, nullptr, w2, nullptr, out, idx, gate, counts, ws, ws_bytes, stream,
+    return forward_impl(s, EXPERTS_BF16, x, wr, bias, w13, nullptr, w2, nullptr, out, idx, gate, counts, ws, ws_bytes, stream,
                         events);
 }
 
@@ -285,7 +319,7 @@ int lc_moe_forward_fp8(const lc_moe_shape* s, const void* x, const void* wr, con
                        const float* w2_scale, void* out, int32_t* idx, float* gate, int32_t* counts,
                        void* ws, size_t ws_bytes, void* stream) {
     if (!w13_scale || !w2_scale) return LC_MOE_ERR_INVALID_ARG;
-    return forward_impl(s, x, wr, bias, w13q, w13_scale, w2q, w2_scale, out, idx, gate, counts, ws,
+    return forward_impl(s, EXPERTS_E4M3, x, wr, bias, w13q, w13_scale, w2q, w2_scale, out, idx, gate, counts, ws,
                         ws_bytes, stream, nullptr);
 }
 
@@ -297,7 +331,7 @@ int lc_moe_forward_fp8_timed(const lc_moe_shape* s, const void* x, const void* w
     if (!w13_scale || !w2_scale || !events) return LC_MOE_ERR_INVALID_ARG;
     for (int i = 0; i <= LC_MOE_NUM_STAGES; ++i)
         if (!events[i]) return LC_MOE_ERR_INVALID_ARG;
-    return forward_impl(s, x, wr, bias, w13q, w13_scale, w2q, w2_scale, out, idx, gate, counts, ws,
+    return forward_impl(s, EXPERTS_E4M3, x, wr, bias, w13q, w13_scale, w2q, w2_scale, out, idx, gate, counts, ws,
                         ws_bytes, stream, events);
 }
 
@@ -492,6 +526,103 @@ int lc_moe_permute_noalloc(const lc_moe_shape* s, const int32_t* idx, const void
                                    status, st));
     if (x_perm) LC_CUDA(launch_gather(x, s->T, s->d, s->K, pair_row, x_perm, status, st));
     return LC_MOE_OK;
+}
+
+int lc_moe_gate(const lc_moe_shape* s, const lc_moe_gate_opts* o, const void* logits, int32_t logits_type,
+                const float* bias, int32_t* idx, float* gate, int32_t* counts, void* ws, size_t ws_bytes,
+                void* stream) {
+    LC_TRY(check_shape(s));
+    if (!o) o = &kDefaultGate;
+    LC_TRY(check_gate(s, o));
+    if (s->T == 0) return LC_MOE_OK;  // empty tensors may be null pointers
+    if (!logits || !idx || !gate || !ws || (logits_type != LC_MOE_F32 && logits_type != LC_MOE_BF16))
+        return LC_MOE_ERR_INVALID_ARG;
+    if (ws_bytes < kStatusBytes) return LC_MOE_ERR_WORKSPACE_TOO_SMALL;
+    const uintptr_t unit = logits_type == LC_MOE_BF16 ? 2 : 4;
+    if (reinterpret_cast<uintptr_t>(logits) % unit || !aligned16(ws)) return LC_MOE_ERR_MISALIGNED;
+    LC_TRY(device_ok());
+    LC_CUDA(launch_gate(logits, logits_type == LC_MOE_BF16, bias, s->T, s->N + s->Z, s->K, *o, idx, gate, counts,
+                        at<uint32_t>(ws, 0), static_cast<cudaStream_t>(stream)));
+    return LC_MOE_OK;
+}
+
+int lc_moe_gate_backward(const lc_moe_shape* s, const lc_moe_gate_opts* o, const void* logits,
+                         int32_t logits_type, const int32_t* idx, const float* dgate, void* dlogits, void* ws,
+                         size_t ws_bytes, void* stream) {
+    LC_TRY(check_shape(s));
+    if (!o) o = &kDefaultGate;
+    LC_TRY(check_gate(s, o));
+    if (s->T == 0) return LC_MOE_OK;  // empty tensors may be null pointers
+    if (!logits || !idx || !dgate || !dlogits || !ws || dlogits == logits ||
+        (logits_type != LC_MOE_F32 && logits_type != LC_MOE_BF16))
+        return LC_MOE_ERR_INVALID_ARG;
+    if (ws_bytes < kStatusBytes) return LC_MOE_ERR_WORKSPACE_TOO_SMALL;
+    const uintptr_t unit = logits_type == LC_MOE_BF16 ? 2 : 4;
+    if (reinterpret_cast<uintptr_t>(logits) % unit || reinterpret_cast<uintptr_t>(dlogits) % unit || !aligned16(ws))
+        return LC_MOE_ERR_MISALIGNED;
+    LC_TRY(device_ok());
+    LC_CUDA(launch_gate_backward(logits, logits_type == LC_MOE_BF16, idx, dgate, s->T, s->N + s->Z, s->K, *o, dlogits,
+                                 at<uint32_t>(ws, 0), static_cast<cudaStream_t>(stream)));
+    return LC_MOE_OK;
+}
+
+int lc_moe_combine_backward(const lc_moe_shape* s, const void* dout, const void* x, const void* y, int64_t y_rows,
+                            const float* gate, const int32_t* pair_row, void* dy, float* dgate, void* dx, void* ws,
+                            size_t ws_bytes, void* stream) {
+    LC_TRY(check_shape(s));
+    if (s->T == 0) return LC_MOE_OK;  // empty tensors may be null pointers
+    if (!dout || !x || !gate || !pair_row || !dgate || !dx || !ws || y_rows < 0 || (y_rows > 0 && (!y || !dy)))
+        return LC_MOE_ERR_INVALID_ARG;
+    if (ws_bytes < kStatusBytes) return LC_MOE_ERR_WORKSPACE_TOO_SMALL;
+    for (const void* p : {dout, x, y, static_cast<const void*>(dy), static_cast<const void*>(dx),
+                          static_cast<const void*>(ws)})
+        if (p && !aligned16(p)) return LC_MOE_ERR_MISALIGNED;
+    LC_TRY(device_ok());
+    LC_CUDA(launch_combine_backward(dout, x, y, y_rows, gate, pair_row, s->T, s->d, s->K, dy, dgate, dx,
+                                    at<uint32_t>(ws, 0), static_cast<cudaStream_t>(stream)));
+    return LC_MOE_OK;
+}
+
+int lc_moe_quantize_w4(const void* src, int64_t rows, int32_t cols, int32_t group, void* codes, void* scale,
+                       void* stream) {
+    if ((group != 32 && group != 64 && group != 128) || rows < 0 || rows % 16 || cols < 64 || cols % 64 || cols % group)
+        return LC_MOE_ERR_INVALID_ARG;
+    if (rows == 0) return LC_MOE_OK;
+    if (!src || !codes || !scale) return LC_MOE_ERR_INVALID_ARG;
+    for (const void* p : {src, static_cast<const void*>(codes), static_cast<const void*>(scale)})
+        if (!aligned16(p)) return LC_MOE_ERR_MISALIGNED;
+    LC_TRY(device_ok());
+    LC_CUDA(launch_quantize_w4(src, rows, cols, group, codes, scale, static_cast<cudaStream_t>(stream)));
+    return LC_MOE_OK;
+}
+
+int lc_moe_expert_ffn_w4(const lc_moe_shape* s, const void* x_perm, const int32_t* offsets, const void* w13q,
+                         const void* w13_scale, const void* w2q, const void* w2_scale, int32_t group, void* h,
+                         void* y, void* ws, size_t ws_bytes, void* stream) {
+    LC_TRY(check_shape(s));
+    LC_TRY(check_group(s, group));
+    if (s->T == 0) return LC_MOE_OK;  // empty tensors may be null pointers
+    if (!x_perm || !offsets || !w13q || !w13_scale || !w2q || !w2_scale || !h || !y || !ws)
+        return LC_MOE_ERR_INVALID_ARG;
+    if (ws_bytes < kStatusBytes) return LC_MOE_ERR_WORKSPACE_TOO_SMALL;
+    for (const void* p : {x_perm, w13q, w13_scale, w2q, w2_scale, static_cast<const void*>(h),
+                          static_cast<const void*>(y), static_cast<const void*>(ws)})
+        if (!aligned16(p)) return LC_MOE_ERR_MISALIGNED;
+    LC_TRY(device_ok());
+    cudaStream_t st = static_cast<cudaStream_t>(stream);
+    const int64_t rows_cap = static_cast<int64_t>(s->T) * s->K;
+    uint32_t* status = at<uint32_t>(ws, 0);
+    LC_CUDA(launch_swiglu_w4(x_perm, rows_cap, offsets, s->N, w13q, w13_scale, group, s->d, s->I, h, status, st));
+    LC_CUDA(launch_down_w4(h, rows_cap, offsets, s->N, w2q, w2_scale, group, s->d, s->I, y, status, st));
+    return LC_MOE_OK;
+}
+
+int lc_moe_forward_w4(const lc_moe_shape* s, const lc_moe_gate_opts* o, const void* x, const void* wr,
+                      const float* bias, const void* w13q, const void* w13_scale, const void* w2q,
+                      const void* w2_scale, int32_t group, void* out, int32_t* idx, float* gate, int32_t* counts,
+                      void* ws, size_t ws_bytes, void* stream) {
+    return forward_impl(s, EXPERTS_W4, x, wr, bias, w13q, w13_scale, w2q, w2_scale, out, idx, gate, counts, ws,
+                        ws_bytes, stream, nullptr, group, o);
 }
 
 }  // extern "C"

@@ -6,6 +6,12 @@
 // One warp per token; each lane owns 8-element (16-byte) column chunks and accumulates in fp32,
 // in rank order, with one fused multiply-add per pick: the zero-expert term costs one read of
 // x_t per token (shared by all its zero picks) and no extra pass.
+//
+// Its gradient, for the same picks:
+//   dgate_{t,r} = sum_c dout_{t,c} v_{t,r,c}
+//   dY[pair_row] = g_{t,r} dout_t                (rows of Y are in one pick each, so none adds up)
+//   dx_t = (sum of the gates of t's zero picks) dout_t
+// with the products and sums in fp32 and one rounding to bf16 at dY and dx.
 #include "common.cuh"
 
 namespace lcmoe {
@@ -95,7 +101,78 @@ __global__ void __launch_bounds__(COMBINE_THREADS)
     }
 }
 
+// One warp per (token, pick).
+__global__ void __launch_bounds__(COMBINE_THREADS)
+    combine_backward_kernel(const uint4* __restrict__ dout, const uint4* __restrict__ x,
+                            const uint4* __restrict__ y, int64_t y_rows, const float* __restrict__ gate,
+                            const int32_t* __restrict__ pair_row, int64_t T, int d8, int K,
+                            uint4* __restrict__ dy, float* __restrict__ dgate, uint4* __restrict__ dx,
+                            uint32_t* __restrict__ status) {
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int64_t warps_total = static_cast<int64_t>(gridDim.x) * (COMBINE_THREADS / 32);
+    for (int64_t it = static_cast<int64_t>(blockIdx.x) * (COMBINE_THREADS / 32) + warp; it < T * (K + 1);
+         it += warps_total) {
+        const int64_t t = it / (K + 1);
+        const int r = static_cast<int>(it - t * (K + 1));
+        const uint4* g8 = dout + t * d8;
+        if (r == K) {  // dx
+            float w = lane < K && pair_row[t * K + lane] < 0 ? gate[t * K + lane] : 0.0f;
+#pragma unroll
+            for (int o = 16; o; o >>= 1) w += __shfl_xor_sync(0xffffffffu, w, o);
+            for (int c = lane; c < d8; c += 32) {
+                float acc[8] = {};
+                fma_row(acc, w, g8[c]);
+                dx[t * d8 + c] = pack8(acc);
+            }
+            continue;
+        }
+        const int32_t row = pair_row[t * K + r];
+        const float w = gate[t * K + r];
+        if (row >= y_rows) {
+            if (lane == 0) {
+                set_status(status, LC_MOE_DEV_IDX_RANGE);
+                dgate[t * K + r] = 0.0f;
+            }
+            continue;
+        }
+        const uint4* v8 = row < 0 ? x + t * d8 : y + row * static_cast<int64_t>(d8);
+        float dot = 0.0f;
+        for (int c = lane; c < d8; c += 32) {
+            const uint4 g = g8[c], v = v8[c];
+            const uint32_t a[4] = {g.x, g.y, g.z, g.w}, b[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                dot = __fmaf_rn(bf16lo(a[j]), bf16lo(b[j]), dot);
+                dot = __fmaf_rn(bf16hi(a[j]), bf16hi(b[j]), dot);
+            }
+            if (row >= 0) {
+                float acc[8] = {};
+                fma_row(acc, w, g);
+                dy[row * static_cast<int64_t>(d8) + c] = pack8(acc);
+            }
+        }
+#pragma unroll
+        for (int o = 16; o; o >>= 1) dot += __shfl_xor_sync(0xffffffffu, dot, o);
+        if (lane == 0) dgate[t * K + r] = dot;
+    }
+}
+
 }  // namespace
+
+cudaError_t launch_combine_backward(const void* dout, const void* x, const void* y, int64_t y_rows,
+                                    const float* gate, const int32_t* pair_row, int T, int d, int K, void* dy,
+                                    float* dgate, void* dx, uint32_t* status, cudaStream_t st) {
+    const DevInfo* di = current_device_info();
+    if (!di) return cudaErrorUnknown;
+    if (T == 0) return cudaSuccess;
+    const int warps = COMBINE_THREADS / 32;
+    int64_t blocks = (static_cast<int64_t>(T) * (K + 1) + warps - 1) / warps;
+    if (blocks > di->sm_count * 8) blocks = di->sm_count * 8;
+    combine_backward_kernel<<<static_cast<int>(blocks), COMBINE_THREADS, 0, st>>>(
+        static_cast<const uint4*>(dout), static_cast<const uint4*>(x), static_cast<const uint4*>(y), y_rows, gate,
+        pair_row, T, d / 8, K, static_cast<uint4*>(dy), dgate, static_cast<uint4*>(dx), status);
+    return cudaGetLastError();
+}
 
 cudaError_t launch_combine(const void* x, const void* y, const float* gate,
                            const int32_t* pair_row, int T, int d, int K, void* out,

@@ -478,6 +478,29 @@ cudaError_t launch_combine(const void* x, const void* y, const float* gate,
                            const int32_t* pair_row, int T, int d, int K, void* out,
                            cudaStream_t st);
 
+// Gradient of the combine (y, dy: y_rows rows).
+cudaError_t launch_combine_backward(const void* dout, const void* x, const void* y, int64_t y_rows,
+                                    const float* gate, const int32_t* pair_row, int T, int d, int K, void* dy,
+                                    float* dgate, void* dx, uint32_t* status, cudaStream_t st);
+
+// General gates and their gradient; bf16: the type of logits and dlogits.
+cudaError_t launch_gate(const void* logits, int bf16, const float* bias, int T, int E, int K,
+                        const lc_moe_gate_opts& o, int32_t* idx, float* gate, int32_t* counts,
+                        uint32_t* status, cudaStream_t st);
+cudaError_t launch_gate_backward(const void* logits, int bf16, const int32_t* idx, const float* dgate, int T,
+                                 int E, int K, const lc_moe_gate_opts& o, void* dlogits, uint32_t* status,
+                                 cudaStream_t st);
+
+// 4-bit experts: quantiser, grouped gate/up product with the SwiGLU epilogue, grouped down product.
+cudaError_t launch_quantize_w4(const void* src, int64_t rows, int cols, int group, void* codes, void* scale,
+                               cudaStream_t st);
+cudaError_t launch_swiglu_w4(const void* x_perm, int64_t rows_cap, const int32_t* offsets, int N, const void* w13q,
+                             const void* w13_scale, int group, int d, int I, void* h, uint32_t* status,
+                             cudaStream_t st);
+cudaError_t launch_down_w4(const void* h, int64_t rows_cap, const int32_t* offsets, int N, const void* w2q,
+                           const void* w2_scale, int group, int d, int I, void* y, uint32_t* status,
+                           cudaStream_t st);
+
 cudaError_t launch_wait_check(uint32_t* status, uint64_t limit_ns, cudaStream_t st);
 
 // Expert parallelism: expert-major permutation of rows received source-major (cnt [G, n_local],

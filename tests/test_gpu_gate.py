@@ -1,0 +1,281 @@
+"""General gates and their gradient on the device, against plain 64-bit forms (tests/operator_ref.py).
+
+Picks have to be equal. Gates: expf is within 2 steps, its argument z - m is rounded once (|z - m|
+half steps relative to the result), the sum and the quotient add a few more, in numerator and
+denominator: (2 R + 64) half steps of fp32 with R the range of a row's logits. Gradients: the same
+factor times the sizes of the terms added (the reference's bound), plus the rounding of a bf16
+result."""
+import math
+
+import numpy as np
+import pytest
+import torch
+
+from mixture_experts_zero_b200 import binding as B
+from tests import operator_ref as R
+
+pytestmark = pytest.mark.gpu
+
+CASES = [
+    # T, E, K, groups, top, rank
+    (1, 1, 1, 1, 1, 1), (1, 768, 12, 1, 1, 1), (37, 12, 3, 4, 2, 2), (64, 33, 7, 1, 1, 1), (5, 2048, 32, 1, 1, 1),
+    (9, 2048, 32, 32, 7, 2), (130, 768, 12, 8, 4, 2), (33, 96, 6, 3, 1, 1), (20, 333, 7, 9, 5, 2), (17, 64, 32, 32, 16, 2),
+    (11, 31, 31, 31, 31, 2), (21, 1025, 9, 1, 1, 1), (13, 40, 8, 8, 8, 1), (700, 130, 5, 2, 1, 2),
+]
+
+
+def logits_of(T, E, seed, bf16, std=2.0):
+    z = torch.from_numpy(np.random.default_rng(seed).standard_normal((T, E)).astype(np.float32) * std)
+    return (z.to(torch.bfloat16) if bf16 else z).cuda()
+
+
+def f64(t):
+    return t.detach().double().cpu().numpy()
+
+
+def span(z):
+    """The range of a row's logits; a logit more than 110 below the largest adds nothing in fp32."""
+    z = np.where(np.isinf(z), 0.0, z)
+    return min(110.0, float((z.max(1) - z.min(1)).max()))
+
+
+def check_gate(z, b, K, N, score, groups=1, top=1, rank=1, renorm=True, scale=1.0, **kw):
+    E = z.shape[1]
+    counts = torch.full((E,), 3, dtype=torch.int32, device="cuda")
+    ws = torch.zeros(256, dtype=torch.uint8, device="cuda")
+    idx, gate = B.lc_moe_gate(z, b, K, N, score=score, groups=groups, top_groups=top, group_rank=rank, renorm=renorm,
+                              scale=scale, counts=counts, ws=ws, **kw)
+    assert B.lc_moe_read_status(ws) == 0
+    s = R.scores(f64(z), score)
+    want = R.picks(s, None if b is None else f64(b), K, groups, top, rank)
+    np.testing.assert_array_equal(idx.cpu().numpy(), want)
+    ref = R.gates(f64(z), s, want, score, renorm, scale)
+    tol = (2 * span(f64(z)) + 64) * R.U32 * np.abs(ref) + 1e-37
+    err = np.abs(f64(gate) - ref)
+    assert np.all(err <= tol), float((err / tol).max())
+    np.testing.assert_array_equal(counts.cpu().numpy() - 3, np.bincount(want.ravel(), minlength=E))
+    return idx, gate
+
+
+@pytest.mark.parametrize("score", ["softmax", "sigmoid"])
+@pytest.mark.parametrize("case", CASES)
+def test_gate_against_64_bits(cuda_device, case, score):
+    T, E, K, groups, top, rank = case
+    rng = np.random.default_rng(hash(case) % 1000)
+    for bf16 in (False, True):
+        z = logits_of(T, E, E + T, bf16)
+        for renorm, scale, bias in ((True, 1.0, True), (False, 2.5, True), (True, 2.5, False)):
+            b = torch.from_numpy((rng.random(E) * 0.2 - 0.1).astype(np.float32)).cuda() if bias else None
+            check_gate(z, b, K, max(1, E // 2), score, groups, top, rank, renorm, scale)
+
+
+@pytest.mark.parametrize("score", ["softmax", "sigmoid"])
+def test_many_tokens(cuda_device, score):
+    """Enough tokens that some have keys closer to each other than fp32 resolves."""
+    z = logits_of(6000, 96, 5, False, std=4.0)
+    b = torch.from_numpy((np.random.default_rng(0).random(96) * 1e-3).astype(np.float32)).cuda()
+    check_gate(z, b, 8, 64, score)
+    check_gate(z, b, 8, 64, score, groups=8, top=3, rank=2, scale=2.5)
+
+
+@pytest.mark.parametrize("score", ["softmax", "sigmoid"])
+def test_keys_that_fp32_cannot_tell_apart(cuda_device, score):
+    """Neighbouring fp32 logits and biases that nearly undo their differences."""
+    rng = np.random.default_rng(3)
+    E, K = 80, 9
+    base = np.float32(1.25) + np.arange(E, dtype=np.float32) * np.float32(2.0 ** -22)
+    z = np.stack([rng.permutation(base) for _ in range(40)]).astype(np.float32)
+    for b in (None, np.zeros(E, np.float32), (rng.integers(-3, 4, E) * 2.0 ** -26).astype(np.float32)):
+        bt = None if b is None else torch.from_numpy(b).cuda()
+        check_gate(torch.from_numpy(z).cuda(), bt, K, 40, score)
+        check_gate(torch.from_numpy(z).cuda(), bt, K, 40, score, groups=8, top=3, rank=2)
+
+
+@pytest.mark.parametrize("score", ["softmax", "sigmoid"])
+def test_ties_go_to_the_lower_index(cuda_device, score):
+    rng = np.random.default_rng(1)
+    for (T, E, K, groups, top, rank) in [(40, 12, 3, 1, 1, 1), (64, 65, 32, 1, 1, 1), (3, 2048, 32, 1, 1, 1),
+                                         (50, 96, 6, 8, 3, 2), (50, 96, 6, 8, 3, 1)]:
+        z = torch.from_numpy(rng.integers(-1, 2, (T, E)).astype(np.float32)).cuda()
+        z[0] = 0.0  # every key equal
+        check_gate(z, None, K, max(1, E // 2), score, groups, top, rank)
+        check_gate(z.to(torch.bfloat16), None, K, max(1, E // 2), score, groups, top, rank, renorm=False)
+
+
+@pytest.mark.parametrize("score", ["softmax", "sigmoid"])
+def test_masked_logits_and_switched_off_experts(cuda_device, score):
+    """-inf and lowest logits, rows that leave nothing, -inf biases, fewer live experts than K."""
+    E, K = 48, 5
+    z = logits_of(9, E, 7, False)
+    z[0, 3:] = -math.inf
+    z[1, :] = -math.inf
+    z[2, 1::2] = torch.finfo(torch.float32).min
+    z[3, :] = torch.finfo(torch.float32).min
+    z[4, :] = -300.0
+    z[4, 7] = -299.0
+    b = torch.zeros(E, device="cuda")
+    for renorm in (True, False):
+        check_gate(z, None, K, 24, score, renorm=renorm)
+        check_gate(z, b, K, 24, score, renorm=renorm, scale=2.5)
+    b[4:] = -math.inf
+    check_gate(z, b, K, 24, score)
+    b[:] = -math.inf
+    check_gate(z, b, K, 24, score)
+    b[:] = 0
+    b[::3] = -math.inf
+    check_gate(z, b, K, 24, score, groups=8, top=3, rank=1)
+    check_gate(z, b, K, 24, score, groups=8, top=3, rank=2)
+
+
+def test_all_masked_row_has_zero_gates(cuda_device):
+    z = torch.full((2, 16), -math.inf, device="cuda")
+    for score in ("softmax", "sigmoid"):
+        for renorm in (True, False):
+            idx, gate = B.lc_moe_gate(z, None, 4, 16, score=score, renorm=renorm)
+            assert gate.eq(0).all() and idx.cpu().tolist() == [[0, 1, 2, 3]] * 2
+            d = B.lc_moe_gate_backward(z, idx, torch.ones(2, 4, device="cuda"), score=score, renorm=renorm)
+            assert d.eq(0).all()
+
+
+def test_extreme_biases(cuda_device):
+    """Biases far larger than the scores, and of both signs: the key is the rounded 64-bit sum."""
+    z = logits_of(30, 64, 2, False)
+    b = torch.from_numpy((np.random.default_rng(5).standard_normal(64) * 1e4).astype(np.float32)).cuda()
+    for score in ("softmax", "sigmoid"):
+        check_gate(z, b, 8, 64, score)
+        check_gate(z, b, 8, 64, score, groups=8, top=2, rank=2)
+        check_gate(z, torch.full((64,), 1e3, device="cuda"), 8, 64, score)
+
+
+def test_nan_keys_are_reported(cuda_device):
+    for bad, score in ((math.nan, "softmax"), (math.nan, "sigmoid"), (math.inf, "softmax")):
+        z = logits_of(6, 40, 1, False)
+        clean = z.clone()
+        z[2, 9] = bad
+        ws = torch.zeros(256, dtype=torch.uint8, device="cuda")
+        idx, gate = B.lc_moe_gate(z, None, 4, 40, score=score, ws=ws)
+        assert B.lc_moe_read_status(ws, raise_on_error=False) == B.DEV_NAN_KEY
+        assert idx[2].cpu().tolist() == [0, 1, 2, 3] and gate[2].isnan().all()
+        ref, rg = B.lc_moe_gate(clean, None, 4, 40, score=score)
+        keep = [0, 1, 3, 4, 5]
+        assert torch.equal(idx[keep], ref[keep]) and torch.equal(gate[keep], rg[keep])
+    z = logits_of(2, 8, 1, False)
+    b = torch.zeros(8, device="cuda")
+    b[0], b[1] = math.inf, -math.inf
+    ws = torch.zeros(256, dtype=torch.uint8, device="cuda")
+    B.lc_moe_gate(z, b, 2, 8, groups=4, top_groups=2, group_rank=2, ws=ws)
+    assert B.lc_moe_read_status(ws, raise_on_error=False) == B.DEV_NAN_KEY
+
+
+def test_infinite_sigmoid_logit_is_a_score_of_one(cuda_device):
+    z = logits_of(3, 20, 4, False)
+    z[1, 5] = math.inf
+    idx, gate = B.lc_moe_gate(z, None, 2, 20, score="sigmoid", renorm=False)
+    assert int(idx[1, 0]) == 5 and float(gate[1, 0]) == 1.0
+
+
+def test_unaligned_rows_and_default_options(cuda_device):
+    """Logits that start on an odd element, and the C call with NULL options."""
+    import ctypes
+    for bf16 in (False, True):
+        z = logits_of(21, 77, 8, bf16)
+        flat = torch.zeros(21 * 77 + 1, dtype=z.dtype, device="cuda")
+        flat[1:] = z.view(-1)
+        v = flat[1:].view(21, 77)
+        idx, gate = check_gate(v, None, 6, 70, "softmax")
+        idx2, gate2 = torch.empty_like(idx), torch.empty_like(gate)
+        ws = torch.zeros(256, dtype=torch.uint8, device="cuda")
+        s = B.Shape(21, 64, 70, 7, 6, 64)
+        rc = B.library().lc_moe_gate(ctypes.byref(s), None, B._ptr(v), int(bf16), None, B._ptr(idx2), B._ptr(gate2),
+                                     None, B._ptr(ws), 256, B._stream(None))
+        torch.cuda.synchronize()
+        assert rc == 0 and torch.equal(idx, idx2) and torch.equal(gate, gate2)
+        d = B.lc_moe_gate_backward(v, idx, torch.ones_like(gate), renorm=False)
+        check_backward(v, idx, torch.ones_like(gate), "softmax", False, 1.0, d)
+
+
+# ------------------------------------------------------------------------------- gradient --
+
+def check_backward(z, idx, dg, score, renorm, scale, got):
+    dz, bound = R.gate_backward(f64(z), idx.cpu().numpy(), f64(dg), score, renorm, scale)
+    tol = (2 * span(f64(z)) + 64) * R.U32 * bound + 1e-37
+    if z.dtype == torch.bfloat16:
+        tol = tol * (1 + R.U16) + R.U16 * np.abs(dz)
+    err = np.abs(f64(got) - dz)
+    assert got.dtype == z.dtype
+    assert np.all(err <= tol), float((err / tol).max())
+
+
+@pytest.mark.parametrize("score", ["softmax", "sigmoid"])
+@pytest.mark.parametrize("renorm", [True, False])
+@pytest.mark.parametrize("T,E,K", [(1, 1, 1), (3, 2048, 32), (77, 333, 7), (257, 768, 12), (50, 12, 12)])
+def test_gate_gradient_against_the_formula(cuda_device, T, E, K, renorm, score):
+    for bf16 in (False, True):
+        z = logits_of(T, E, T + E, bf16)
+        idx, gate = B.lc_moe_gate(z, None, K, E, score=score, renorm=renorm, scale=1.5)
+        dg = torch.from_numpy(np.random.default_rng(K).standard_normal((T, K)).astype(np.float32)).cuda()
+        out = torch.full_like(z, 7.0)
+        got = B.lc_moe_gate_backward(z, idx, dg, score=score, renorm=renorm, scale=1.5, dlogits=out)
+        assert got is out
+        check_backward(z, idx, dg, score, renorm, 1.5, got)
+
+
+@pytest.mark.parametrize("score", ["softmax", "sigmoid"])
+@pytest.mark.parametrize("renorm", [True, False])
+def test_gate_gradient_against_differences(cuda_device, renorm, score):
+    """Central differences of the 64-bit gates with the picks held fixed: their error is h^2 / 6 times
+    a third derivative (below 8 for scores in 0..1 and quotients of them), 2e-6 at h = 1e-3."""
+    T, E, K = 4, 24, 5
+    z = logits_of(T, E, 11, False, std=1.0)
+    idx, _ = B.lc_moe_gate(z, None, K, E, score=score, renorm=renorm)
+    dg = torch.from_numpy(np.random.default_rng(2).standard_normal((T, K)).astype(np.float32)).cuda()
+    got = f64(B.lc_moe_gate_backward(z, idx, dg, score=score, renorm=renorm))
+    z64, i, w = f64(z), idx.cpu().numpy(), f64(dg)
+    h = 1e-3
+
+    def total(zz):
+        return (R.gates(zz, R.scores(zz, score), i, score, renorm, 1.0) * w).sum(1)
+    for e in range(E):
+        up, down = z64.copy(), z64.copy()
+        up[:, e] += h
+        down[:, e] -= h
+        diff = (total(up) - total(down)) / (2 * h)
+        assert np.abs(got[:, e] - diff).max() <= 2e-6 * np.abs(w).sum(1).max() + 1e-6
+
+
+def test_gate_gradient_repeated_and_bad_picks(cuda_device):
+    z = logits_of(4, 30, 3, False)
+    idx = torch.tensor([[1, 1, 5, 1], [0, 29, 0, 29], [2, -1, 30, 4], [7, 8, 9, 10]], dtype=torch.int32, device="cuda")
+    dg = torch.from_numpy(np.random.default_rng(9).standard_normal((4, 4)).astype(np.float32)).cuda()
+    for score in ("softmax", "sigmoid"):
+        for renorm in (True, False):
+            ws = torch.zeros(256, dtype=torch.uint8, device="cuda")
+            got = B.lc_moe_gate_backward(z, idx, dg, score=score, renorm=renorm, ws=ws)
+            assert B.lc_moe_read_status(ws, raise_on_error=False) == B.DEV_IDX_RANGE
+            check_backward(z, idx, dg, score, renorm, 1.0, got)
+
+
+def test_gate_on_another_stream_and_in_a_graph(cuda_device):
+    z = logits_of(300, 96, 1, False)
+    b = torch.linspace(-0.1, 0.1, 96, device="cuda")
+    kw = dict(score="sigmoid", groups=8, top_groups=4, group_rank=2, scale=2.5)
+    want = B.lc_moe_gate(z, b, 6, 64, **kw)
+    dg = torch.ones(300, 6, device="cuda")
+    want_d = B.lc_moe_gate_backward(z, want[0], dg, score="softmax", renorm=False)
+    torch.cuda.synchronize()
+    st = torch.cuda.Stream()
+    got = B.lc_moe_gate(z, b, 6, 64, stream=st, **kw)
+    got_d = B.lc_moe_gate_backward(z, got[0], dg, score="softmax", renorm=False, stream=st)
+    st.synchronize()
+    assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1]) and torch.equal(got_d, want_d)
+    idx, gate, d = torch.zeros_like(want[0]), torch.zeros_like(want[1]), torch.zeros_like(z)
+    ws = torch.zeros(256, dtype=torch.uint8, device="cuda")
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        B.lc_moe_gate(z, b, 6, 64, idx=idx, gate=gate, ws=ws, **kw)
+        B.lc_moe_gate_backward(z, idx, dg, score="softmax", renorm=False, dlogits=d, ws=ws)
+    for _ in range(2):
+        idx.zero_(), gate.zero_(), d.zero_()
+        g.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(idx, want[0]) and torch.equal(gate, want[1]) and torch.equal(d, want_d)
