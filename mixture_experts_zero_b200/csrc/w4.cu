@@ -46,7 +46,7 @@ __device__ __forceinline__ uint32_t codes_bf16x2(uint32_t w) {
 // D += A B, m16n8k16, bf16 operands, fp32 accumulators
 __device__ __forceinline__ void mma16816(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3,
                                          uint32_t b0, uint32_t b1) {
-    asm volatile(
+    asm(
         "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
         "{%0, %1, %2, %3};"
         : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
@@ -130,43 +130,100 @@ struct W4Args {
     const int32_t* offsets;      // [N + 1] row offsets of the experts
     const __nv_bfloat16* x;      // [rows_cap, k] grouped rows
     const uint8_t* codes;        // [N][m / 16][k / 64][512]
-    const uint32_t* scale;       // [N][m / 16][k / group][8] row pairs
+    const uint8_t* scale;        // [N][m / 16][k / group][32]
     __nv_bfloat16* out;          // [rows_cap, n_out]
     uint32_t* status;
     int64_t rows_cap;
     int N, k, m, n_out, group;   // m: weight rows of an expert (2I or d)
+    int split;                   // warps that share a tile's reduction (1, 2, 4 or 8)
 };
 
-constexpr int W4_THREADS = 256;
-constexpr int RED = 68;  // padded feature stride of the partial sums
+constexpr int W4_WARPS = 8;
+constexpr int W4_THREADS = 32 * W4_WARPS;
+constexpr int TOK = 16;                       // rows of an expert per item
+constexpr int STAGES = 4;                     // ring depth of each warp
+constexpr int STAGE_BYTES = 4 * 512 + 2 * 128;  // codes of 4 blocks of 16 rows x 64 columns, their scales
+constexpr int RED = 68;                       // padded feature stride of the partial sums
+constexpr int RED_WARP = 8 * RED;             // floats of one warp's partial sums (8 rows x 64 features)
+constexpr size_t RING_BYTES = static_cast<size_t>(W4_WARPS) * STAGES * STAGE_BYTES;
+constexpr size_t RED_BYTES = 2ull * W4_WARPS * RED_WARP * 4;
 
-// Item: 64 weight rows of one expert (32 gate and 32 up rows, or 64 output features) times up to 8
-// of its rows. A CTA's 8 warps split the reduction and join their sums in shared memory.
-template <bool SWIGLU>
-__global__ void __launch_bounds__(W4_THREADS) w4_kernel(const W4Args a) {
-    extern __shared__ uint8_t s_raw[];
-    float* red = reinterpret_cast<float*>(s_raw);                          // [8][8][RED]
-    int64_t* pre = reinterpret_cast<int64_t*>(s_raw + 8 * 8 * RED * 4);    // [N + 1] item prefix sums
+__device__ __forceinline__ void cp_async16(uint32_t dst, const void* src) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+}
+__device__ __forceinline__ void cp_async4(uint32_t dst, const void* src) {
+    asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(dst), "l"(src) : "memory");
+}
+__device__ __forceinline__ void cp_async_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void cp_async_wait() {
+    asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
+
+// One step of 64 columns of a warp: 64 weight rows from the ring times NT tiles of 8 rows.
+template <int NT, bool G32>
+__device__ __forceinline__ void w4_step(const uint8_t* stage, int lane, const uint4 (&xv)[2][2], float (&acc)[4][2][4]) {
+    const int g = lane >> 2;
+#pragma unroll
+    for (int b = 0; b < 4; ++b) {
+        const uint4 w = *reinterpret_cast<const uint4*>(stage + b * 512 + lane * 16);
+        const uint32_t wr[2][2] = {{w.x, w.y}, {w.z, w.w}};
+        float s4[NT][4];
+#pragma unroll
+        for (int G = 0; G < 2; ++G) {
+            const uint32_t a0 = codes_bf16x2<0>(wr[G][0]), a1 = codes_bf16x2<0>(wr[G][1]);
+            const uint32_t a2 = codes_bf16x2<1>(wr[G][0]), a3 = codes_bf16x2<1>(wr[G][1]);
+            const uint32_t a4 = codes_bf16x2<2>(wr[G][0]), a5 = codes_bf16x2<2>(wr[G][1]);
+            const uint32_t a6 = codes_bf16x2<3>(wr[G][0]), a7 = codes_bf16x2<3>(wr[G][1]);
+#pragma unroll
+            for (int n = 0; n < NT; ++n) {
+                if (G == 0 || G32) {
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) s4[n][i] = 0.0f;
+                }
+                mma16816(s4[n], a0, a1, a2, a3, xv[n][G].x, xv[n][G].y);
+                mma16816(s4[n], a4, a5, a6, a7, xv[n][G].z, xv[n][G].w);
+            }
+            if (G == 1 || G32) {
+                const uint32_t sc = *reinterpret_cast<const uint32_t*>(stage + 2048 + (G32 ? G * 128 : 0) + b * 32 + g * 4);
+#pragma unroll
+                for (int n = 0; n < NT; ++n) {
+                    acc[b][n][0] = fmaf(bf16lo(sc), s4[n][0], acc[b][n][0]);
+                    acc[b][n][1] = fmaf(bf16lo(sc), s4[n][1], acc[b][n][1]);
+                    acc[b][n][2] = fmaf(bf16hi(sc), s4[n][2], acc[b][n][2]);
+                    acc[b][n][3] = fmaf(bf16hi(sc), s4[n][3], acc[b][n][3]);
+                }
+            }
+        }
+    }
+}
+
+// Item: `8 / split` tiles of 64 weight rows of one expert (32 gate and 32 up rows, or 64 output
+// features) times up to 16 of its rows. The CTA's warps form 8 / split teams, one for each tile; a
+// team's warps take every split-th step of 64 columns and join their sums in shared memory. Each
+// warp streams its codes and scales through a ring of its own (cp.async, no barriers), which runs
+// on across items; the activations of the next step are loaded into registers a step ahead.
+template <bool SWIGLU, bool G32>
+__global__ void __launch_bounds__(W4_THREADS, 2) w4_kernel(const W4Args a) {
+    extern __shared__ __align__(128) uint8_t s_raw[];
+    float* red = reinterpret_cast<float*>(s_raw + RING_BYTES);
+    int32_t* pre = reinterpret_cast<int32_t*>(s_raw + RING_BYTES + RED_BYTES);  // [N + 1] row-tile prefix sums
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int g = lane >> 2, t = lane & 3;
-    const int tiles = a.m / 64;
     if (warp == 0) {
-        int64_t run = 0;
+        int run = 0;
         if (lane == 0) pre[0] = 0;
         for (int base = 0; base < a.N; base += 32) {
             const int e = base + lane;
-            int64_t n = 0;
+            int n = 0;
             if (e < a.N) {
-                int cnt = a.offsets[e + 1] - a.offsets[e];
-                if (a.offsets[e] < 0 || cnt < 0 || a.offsets[e + 1] > a.rows_cap) {
-                    cnt = 0;
-                    set_status(a.status, LC_MOE_DEV_IDX_RANGE);
-                }
-                n = static_cast<int64_t>((cnt + 7) / 8) * tiles;
+                const int lo = a.offsets[e], hi = a.offsets[e + 1];
+                if (lo < 0 || hi < lo || hi > a.rows_cap) set_status(a.status, LC_MOE_DEV_IDX_RANGE);
+                else n = (hi - lo + TOK - 1) / TOK;
             }
 #pragma unroll
             for (int o = 1; o < 32; o <<= 1) {
-                const int64_t v = __shfl_up_sync(FULL, n, o);
+                const int v = __shfl_up_sync(FULL, n, o);
                 if (lane >= o) n += v;
             }
             if (e < a.N) pre[e + 1] = run + n;
@@ -174,86 +231,181 @@ __global__ void __launch_bounds__(W4_THREADS) w4_kernel(const W4Args a) {
         }
     }
     __syncthreads();
-    const int64_t total = pre[a.N];
+    const int tiles = a.m / 64, teams = W4_WARPS / a.split;
+    const int team = warp / a.split, kw = warp % a.split;
+    const int super = (tiles + teams - 1) / teams;  // items per 16 rows of an expert
+    const int64_t total = static_cast<int64_t>(pre[a.N]) * super;
     const int nk = a.k / 64, ngrp = a.k / a.group;
-    for (int64_t item = blockIdx.x; item < total; item += gridDim.x) {
+    const int64_t blk_codes = static_cast<int64_t>(nk) * 512, blk_scale = static_cast<int64_t>(ngrp) * 32;
+    const int64_t mblk = a.m / 16;
+
+    struct Item {
+        int64_t row0;  // first row
+        int rows;      // 1..16
+        int e, tile;
+    };
+    auto locate = [&](int64_t item) {
+        const int rt = static_cast<int>(item / super);
         int lo = 0, hi = a.N - 1;
         while (lo < hi) {
             const int mid = (lo + hi + 1) >> 1;
-            if (pre[mid] <= item) lo = mid;
+            if (pre[mid] <= rt) lo = mid;
             else hi = mid - 1;
         }
-        const int e = lo;
-        const int64_t local = item - pre[e];
-        const int tile = static_cast<int>(local % tiles);
-        const int64_t row0 = a.offsets[e] + (local / tiles) * 8;
-        const int rows = static_cast<int>(min(static_cast<int64_t>(8), a.offsets[e + 1] - row0));
-        // weight row blocks (16 rows) of this item: SwiGLU takes two of the gate and two of the up rows
-        const int64_t mblk = a.m / 16;
-        int blk[4];
+        Item it;
+        it.e = lo;
+        it.tile = static_cast<int>(item - static_cast<int64_t>(rt) * super) * teams + team;
+        it.row0 = __ldg(a.offsets + lo) + static_cast<int64_t>(rt - pre[lo]) * TOK;
+        it.rows = static_cast<int>(min(static_cast<int64_t>(TOK), __ldg(a.offsets + lo + 1) - it.row0));
+        return it;
+    };
+    // 16-row weight blocks of a tile: SwiGLU takes two of the gate rows and two of the up rows
+    auto block_of = [&](int tile, int b) {
+        return SWIGLU ? (b >> 1) * static_cast<int>(mblk / 2) + tile * 2 + (b & 1) : tile * 4 + b;
+    };
+
+    // ---- ring: the producer runs STAGES - 1 steps ahead of the consumer
+    const uint32_t ring = smem_u32(s_raw) + warp * STAGES * STAGE_BYTES;
+    int64_t p_item = blockIdx.x;
+    int p_ks = nk, p_slot = 0;
+    const uint8_t *p_codes = nullptr, *p_scale = nullptr;
+    int64_t p_up = 0;
+    auto produce = [&]() {
+        while (p_ks >= nk && p_item < total) {  // next item in which this warp's team has a tile
+            const Item it = locate(p_item);
+            p_item += gridDim.x;
+            if (it.tile >= tiles) continue;
+            p_ks = kw;
+            const int64_t first = it.e * mblk + block_of(it.tile, 0);
+            p_codes = a.codes + first * blk_codes + static_cast<int64_t>(kw) * 512 + lane * 16;
+            p_up = SWIGLU ? (mblk / 2) * blk_codes : 2 * blk_codes;
+            // lane (g, t) fetches block t's scales of rows g and g + 8
+            p_scale = a.scale + (it.e * mblk + block_of(it.tile, t)) * blk_scale + g * 4;
+        }
+        if (p_ks < nk) {
+            const uint32_t dst = ring + p_slot * STAGE_BYTES;
+            cp_async16(dst + lane * 16, p_codes);
+            cp_async16(dst + 512 + lane * 16, p_codes + blk_codes);
+            cp_async16(dst + 1024 + lane * 16, p_codes + p_up);
+            cp_async16(dst + 1536 + lane * 16, p_codes + p_up + blk_codes);
+            const uint8_t* sc = p_scale + static_cast<int64_t>(p_ks * 64 / a.group) * 32;
+            cp_async4(dst + 2048 + t * 32 + g * 4, sc);
+            if (G32) cp_async4(dst + 2176 + t * 32 + g * 4, sc + 32);
+            p_codes += a.split * 512;
+            p_ks += a.split;
+            p_slot = p_slot + 1 == STAGES ? 0 : p_slot + 1;
+        }
+        cp_async_commit();
+    };
 #pragma unroll
-        for (int b = 0; b < 4; ++b)
-            blk[b] = SWIGLU ? (b >> 1) * (a.m / 32) + tile * 2 + (b & 1) : tile * 4 + b;
-        const __nv_bfloat16* xr = a.x + (row0 + g) * a.k + 8 * t;
-        float acc[4][4] = {};
-        for (int ks = warp; ks < nk; ks += 8) {
-            uint4 xv[2];
+    for (int i = 0; i < STAGES - 1; ++i) produce();
+
+    uint4 xn[2][2];
+    auto load_x = [&](const Item& it, int ks) {
+#pragma unroll
+        for (int n = 0; n < 2; ++n)
 #pragma unroll
             for (int G = 0; G < 2; ++G)
-                xv[G] = g < rows ? *reinterpret_cast<const uint4*>(xr + ks * 64 + 32 * G) : make_uint4(0, 0, 0, 0);
+                xn[n][G] = g + 8 * n < it.rows
+                               ? __ldg(reinterpret_cast<const uint4*>(a.x + (it.row0 + g + 8 * n) * a.k + ks * 64 + 32 * G + 8 * t))
+                               : make_uint4(0, 0, 0, 0);
+    };
+    Item it{}, nx{};
+    if (static_cast<int64_t>(blockIdx.x) < total) {
+        nx = locate(blockIdx.x);
+        load_x(nx, kw);
+    }
+    int slot = 0, buf = 0;
+    for (int64_t item = blockIdx.x; item < total; item += gridDim.x) {
+        it = nx;
+        const bool more = item + gridDim.x < total;
+        if (more) nx = locate(item + gridDim.x);
+        const bool mine = it.tile < tiles;
+        float acc[4][2][4];
+#pragma unroll
+        for (int b = 0; b < 4; ++b)
+#pragma unroll
+            for (int n = 0; n < 2; ++n)
+#pragma unroll
+                for (int i = 0; i < 4; ++i) acc[b][n][i] = 0.0f;
+        if (mine) {
+            for (int ks = kw; ks < nk; ks += a.split) {
+                uint4 xv[2][2];
+#pragma unroll
+                for (int n = 0; n < 2; ++n)
+#pragma unroll
+                    for (int G = 0; G < 2; ++G) xv[n][G] = xn[n][G];
+                if (ks + a.split < nk) load_x(it, ks + a.split);
+                else if (more) load_x(nx, kw);
+                cp_async_wait<STAGES - 2>();
+                __syncwarp();  // the stage is visible, and the slot before it has been read by every lane
+                const uint8_t* stage = s_raw + (warp * STAGES + slot) * STAGE_BYTES;
+                produce();
+                if (it.rows > 8) w4_step<2, G32>(stage, lane, xv, acc);
+                else w4_step<1, G32>(stage, lane, xv, acc);
+                slot = slot + 1 == STAGES ? 0 : slot + 1;
+            }
+        } else if (more) {
+            load_x(nx, kw);
+        }
+        // join the team's partial sums, 8 rows at a time (two buffers: one barrier each)
+        const int parts = it.rows > 8 ? 2 : 1;
+#pragma unroll
+        for (int n = 0; n < 2; ++n) {
+            if (n >= parts) break;
+            float* r = red + buf * W4_WARPS * RED_WARP;
+            float* w = r + warp * RED_WARP;
 #pragma unroll
             for (int b = 0; b < 4; ++b) {
-                const int64_t bb = e * mblk + blk[b];
-                const uint4 w = *reinterpret_cast<const uint4*>(a.codes + ((bb * nk + ks) * 32 + lane) * 16);
-                const uint32_t wr[2][2] = {{w.x, w.y}, {w.z, w.w}};
-#pragma unroll
-                for (int G = 0; G < 2; ++G) {
-                    float s4[4] = {};
-                    mma16816(s4, codes_bf16x2<0>(wr[G][0]), codes_bf16x2<0>(wr[G][1]), codes_bf16x2<1>(wr[G][0]),
-                             codes_bf16x2<1>(wr[G][1]), xv[G].x, xv[G].y);
-                    mma16816(s4, codes_bf16x2<2>(wr[G][0]), codes_bf16x2<2>(wr[G][1]), codes_bf16x2<3>(wr[G][0]),
-                             codes_bf16x2<3>(wr[G][1]), xv[G].z, xv[G].w);
-                    const uint32_t sc = a.scale[(bb * ngrp + (ks * 64 + 32 * G) / a.group) * 8 + g];
-                    acc[b][0] += bf16lo(sc) * s4[0];
-                    acc[b][1] += bf16lo(sc) * s4[1];
-                    acc[b][2] += bf16hi(sc) * s4[2];
-                    acc[b][3] += bf16hi(sc) * s4[3];
+                w[(2 * t) * RED + 16 * b + g] = acc[b][n][0];
+                w[(2 * t + 1) * RED + 16 * b + g] = acc[b][n][1];
+                w[(2 * t) * RED + 16 * b + g + 8] = acc[b][n][2];
+                w[(2 * t + 1) * RED + 16 * b + g + 8] = acc[b][n][3];
+            }
+            __syncthreads();
+            if (mine) {
+                constexpr int FEAT = SWIGLU ? 32 : 64;
+                const float* s = r + team * a.split * RED_WARP;
+                for (int i = kw * 32 + lane; i < 8 * FEAT; i += a.split * 32) {
+                    const int row = i / FEAT, f = i % FEAT;
+                    if (8 * n + row < it.rows) {
+                        float p = 0.0f, q = 0.0f;
+                        for (int k = 0; k < a.split; ++k) {
+                            p += s[k * RED_WARP + row * RED + f];
+                            if (SWIGLU) q += s[k * RED_WARP + row * RED + 32 + f];
+                        }
+                        a.out[(it.row0 + 8 * n + row) * a.n_out + it.tile * FEAT + f] =
+                            __float2bfloat16_rn(SWIGLU ? silu_mul(p, q) : p);
+                    }
                 }
             }
+            buf ^= 1;
         }
-        float* mine = red + warp * 8 * RED;
-#pragma unroll
-        for (int b = 0; b < 4; ++b) {
-            mine[(2 * t) * RED + 16 * b + g] = acc[b][0];
-            mine[(2 * t + 1) * RED + 16 * b + g] = acc[b][1];
-            mine[(2 * t) * RED + 16 * b + g + 8] = acc[b][2];
-            mine[(2 * t + 1) * RED + 16 * b + g + 8] = acc[b][3];
-        }
-        __syncthreads();
-        constexpr int FEAT = SWIGLU ? 32 : 64;
-        for (int i = threadIdx.x; i < 8 * FEAT; i += W4_THREADS) {
-            const int n = i / FEAT, f = i % FEAT;
-            if (n < rows) {
-                float p = 0.0f, q = 0.0f;
-#pragma unroll
-                for (int w = 0; w < 8; ++w) {
-                    p += red[(w * 8 + n) * RED + f];
-                    if (SWIGLU) q += red[(w * 8 + n) * RED + 32 + f];
-                }
-                a.out[(row0 + n) * a.n_out + tile * FEAT + f] = __float2bfloat16_rn(SWIGLU ? silu_mul(p, q) : p);
-            }
-        }
-        __syncthreads();
     }
+    cp_async_wait<0>();
+}
+
+template <bool SWIGLU, bool G32>
+cudaError_t launch_w4_t(const W4Args& a, cudaStream_t st) {
+    const DevInfo* di = current_device_info();
+    if (!di) return cudaErrorUnknown;
+    static PerDeviceOnce setup;
+    const cudaError_t e = setup.run([](int) {
+        return cudaFuncSetAttribute(w4_kernel<SWIGLU, G32>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                    static_cast<int>(RING_BYTES + RED_BYTES + 2049 * 4));
+    });
+    if (e != cudaSuccess) return e;
+    const size_t smem = RING_BYTES + RED_BYTES + (static_cast<size_t>(a.N) + 1) * 4;
+    w4_kernel<SWIGLU, G32><<<di->sm_count * 2, W4_THREADS, smem, st>>>(a);
+    return cudaGetLastError();
 }
 
 template <bool SWIGLU>
-cudaError_t launch_w4(const W4Args& a, cudaStream_t st) {
-    const DevInfo* di = current_device_info();
-    if (!di) return cudaErrorUnknown;
-    const size_t smem = 8 * 8 * RED * 4 + (static_cast<size_t>(a.N) + 1) * 8;
-    w4_kernel<SWIGLU><<<di->sm_count * 4, W4_THREADS, smem, st>>>(a);
-    return cudaGetLastError();
+cudaError_t launch_w4(W4Args a, cudaStream_t st) {
+    // as many warps on a tile's reduction as leave each of them 8 steps of 64 columns
+    a.split = W4_WARPS;
+    while (a.split > 1 && a.k / 64 / a.split < 8) a.split /= 2;
+    return a.group == 32 ? launch_w4_t<SWIGLU, true>(a, st) : launch_w4_t<SWIGLU, false>(a, st);
 }
 
 }  // namespace
@@ -275,8 +427,8 @@ cudaError_t launch_swiglu_w4(const void* x_perm, int64_t rows_cap, const int32_t
                              const void* w13_scale, int group, int d, int I, void* h, uint32_t* status,
                              cudaStream_t st) {
     W4Args a{offsets, static_cast<const __nv_bfloat16*>(x_perm), static_cast<const uint8_t*>(w13q),
-             static_cast<const uint32_t*>(w13_scale), static_cast<__nv_bfloat16*>(h), status, rows_cap,
-             N, d, 2 * I, I, group};
+             static_cast<const uint8_t*>(w13_scale), static_cast<__nv_bfloat16*>(h), status, rows_cap,
+             N, d, 2 * I, I, group, 0};
     return launch_w4<true>(a, st);
 }
 
@@ -284,8 +436,8 @@ cudaError_t launch_down_w4(const void* h, int64_t rows_cap, const int32_t* offse
                            const void* w2_scale, int group, int d, int I, void* y, uint32_t* status,
                            cudaStream_t st) {
     W4Args a{offsets, static_cast<const __nv_bfloat16*>(h), static_cast<const uint8_t*>(w2q),
-             static_cast<const uint32_t*>(w2_scale), static_cast<__nv_bfloat16*>(y), status, rows_cap,
-             N, I, d, d, group};
+             static_cast<const uint8_t*>(w2_scale), static_cast<__nv_bfloat16*>(y), status, rows_cap,
+             N, I, d, d, group, 0};
     return launch_w4<false>(a, st);
 }
 
