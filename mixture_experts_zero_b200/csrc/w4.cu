@@ -40,17 +40,18 @@ __device__ __forceinline__ uint32_t sub_bf16x2(uint32_t a, uint32_t b) {
 // nibbles p and p + 4 of a word as two bf16 values n - 8
 template <int P>
 __device__ __forceinline__ uint32_t codes_bf16x2(uint32_t w) {
-    return sub_bf16x2(((w >> (4 * P)) & 0x000f000fu) | 0x43004300u, 0x43084308u);
+    uint32_t v;  // (w >> 4 P) & 0x000f000f | 0x43004300 in one logic operation
+    asm("lop3.b32 %0, %1, %2, %3, 0xEA;" : "=r"(v) : "r"(w >> (4 * P)), "r"(0x000f000fu), "r"(0x43004300u));
+    return sub_bf16x2(v, 0x43084308u);
 }
 
-// D += A B, m16n8k16, bf16 operands, fp32 accumulators
+// D = A B + C, m16n8k16, bf16 operands, fp32 accumulators
 __device__ __forceinline__ void mma16816(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3,
-                                         uint32_t b0, uint32_t b1) {
-    asm(
-        "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
-        "{%0, %1, %2, %3};"
-        : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
-        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+                                         uint32_t b0, uint32_t b1, float c0, float c1, float c2, float c3) {
+    asm("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
+        "{%10, %11, %12, %13};"
+        : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
+        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(c0), "f"(c1), "f"(c2), "f"(c3));
 }
 
 __device__ __forceinline__ float silu_mul(float g, float u) { return __fdividef(g, 1.0f + __expf(-g)) * u; }
@@ -140,11 +141,10 @@ struct W4Args {
 
 constexpr int W4_WARPS = 8;
 constexpr int W4_THREADS = 32 * W4_WARPS;
-constexpr int TOK = 16;                       // rows of an expert per item
-constexpr int STAGES = 4;                     // ring depth of each warp
+constexpr int STAGES = 4;                       // ring depth of each warp (even)
 constexpr int STAGE_BYTES = 4 * 512 + 2 * 128;  // codes of 4 blocks of 16 rows x 64 columns, their scales
-constexpr int RED = 68;                       // padded feature stride of the partial sums
-constexpr int RED_WARP = 8 * RED;             // floats of one warp's partial sums (8 rows x 64 features)
+constexpr int RED = 68;                         // padded feature stride of the partial sums
+constexpr int RED_WARP = 8 * RED;               // floats of one warp's partial sums (8 rows x 64 features)
 constexpr size_t RING_BYTES = static_cast<size_t>(W4_WARPS) * STAGES * STAGE_BYTES;
 constexpr size_t RED_BYTES = 2ull * W4_WARPS * RED_WARP * 4;
 
@@ -160,9 +160,10 @@ __device__ __forceinline__ void cp_async_wait() {
     asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
 }
 
-// One step of 64 columns of a warp: 64 weight rows from the ring times NT tiles of 8 rows.
-template <int NT, bool G32>
-__device__ __forceinline__ void w4_step(const uint8_t* stage, int lane, const uint4 (&xv)[2][2], float (&acc)[4][2][4]) {
+// A ring stage (64 weight rows x 64 columns) times NT tiles of 8 rows.
+template <int NT, int MAXNT, bool G32>
+__device__ __forceinline__ void w4_stage(const uint8_t* stage, int lane, const uint4 (&xv)[MAXNT][2],
+                                         float (*acc)[MAXNT][4]) {
     const int g = lane >> 2;
 #pragma unroll
     for (int b = 0; b < 4; ++b) {
@@ -177,12 +178,9 @@ __device__ __forceinline__ void w4_step(const uint8_t* stage, int lane, const ui
             const uint32_t a6 = codes_bf16x2<3>(wr[G][0]), a7 = codes_bf16x2<3>(wr[G][1]);
 #pragma unroll
             for (int n = 0; n < NT; ++n) {
-                if (G == 0 || G32) {
-#pragma unroll
-                    for (int i = 0; i < 4; ++i) s4[n][i] = 0.0f;
-                }
-                mma16816(s4[n], a0, a1, a2, a3, xv[n][G].x, xv[n][G].y);
-                mma16816(s4[n], a4, a5, a6, a7, xv[n][G].z, xv[n][G].w);
+                if (G == 0 || G32) mma16816(s4[n], a0, a1, a2, a3, xv[n][G].x, xv[n][G].y, 0.0f, 0.0f, 0.0f, 0.0f);
+                else mma16816(s4[n], a0, a1, a2, a3, xv[n][G].x, xv[n][G].y, s4[n][0], s4[n][1], s4[n][2], s4[n][3]);
+                mma16816(s4[n], a4, a5, a6, a7, xv[n][G].z, xv[n][G].w, s4[n][0], s4[n][1], s4[n][2], s4[n][3]);
             }
             if (G == 1 || G32) {
                 const uint32_t sc = *reinterpret_cast<const uint32_t*>(stage + 2048 + (G32 ? G * 128 : 0) + b * 32 + g * 4);
@@ -198,13 +196,19 @@ __device__ __forceinline__ void w4_step(const uint8_t* stage, int lane, const ui
     }
 }
 
-// Item: `8 / split` tiles of 64 weight rows of one expert (32 gate and 32 up rows, or 64 output
-// features) times up to 16 of its rows. The CTA's warps form 8 / split teams, one for each tile; a
-// team's warps take every split-th step of 64 columns and join their sums in shared memory. Each
-// warp streams its codes and scales through a ring of its own (cp.async, no barriers), which runs
-// on across items; the activations of the next step are loaded into registers a step ahead.
-template <bool SWIGLU, bool G32>
+template <int V>
+struct Int {
+    static constexpr int value = V;
+};
+
+// Item: `8 / split` tiles of 64 HALVES weight rows of one expert (as many gate as up rows, or output
+// features) times up to 8 MAXNT of its rows. The CTA's warps form 8 / split teams, one for each
+// tile; a team's warps take every split-th step of 64 columns and join their sums in shared memory.
+// Each warp streams its codes and scales through a ring of its own (cp.async, no barriers), which
+// runs on across items; the activations of the next step are loaded into registers a step ahead.
+template <bool SWIGLU, bool G32, int HALVES, int MAXNT>
 __global__ void __launch_bounds__(W4_THREADS, 2) w4_kernel(const W4Args a) {
+    constexpr int TOK = 8 * MAXNT;
     extern __shared__ __align__(128) uint8_t s_raw[];
     float* red = reinterpret_cast<float*>(s_raw + RING_BYTES);
     int32_t* pre = reinterpret_cast<int32_t*>(s_raw + RING_BYTES + RED_BYTES);  // [N + 1] row-tile prefix sums
@@ -231,17 +235,16 @@ __global__ void __launch_bounds__(W4_THREADS, 2) w4_kernel(const W4Args a) {
         }
     }
     __syncthreads();
-    const int tiles = a.m / 64, teams = W4_WARPS / a.split;
+    const int tiles = a.m / (64 * HALVES), teams = W4_WARPS / a.split;
     const int team = warp / a.split, kw = warp % a.split;
-    const int super = (tiles + teams - 1) / teams;  // items per 16 rows of an expert
+    const int super = (tiles + teams - 1) / teams;  // items per row tile of an expert
     const int64_t total = static_cast<int64_t>(pre[a.N]) * super;
     const int nk = a.k / 64, ngrp = a.k / a.group;
     const int64_t blk_codes = static_cast<int64_t>(nk) * 512, blk_scale = static_cast<int64_t>(ngrp) * 32;
     const int64_t mblk = a.m / 16;
 
     struct Item {
-        int64_t row0;  // first row
-        int rows;      // 1..16
+        int row0, rows;  // first row, 1..TOK rows
         int e, tile;
     };
     auto locate = [&](int64_t item) {
@@ -255,112 +258,162 @@ __global__ void __launch_bounds__(W4_THREADS, 2) w4_kernel(const W4Args a) {
         Item it;
         it.e = lo;
         it.tile = static_cast<int>(item - static_cast<int64_t>(rt) * super) * teams + team;
-        it.row0 = __ldg(a.offsets + lo) + static_cast<int64_t>(rt - pre[lo]) * TOK;
-        it.rows = static_cast<int>(min(static_cast<int64_t>(TOK), __ldg(a.offsets + lo + 1) - it.row0));
+        it.row0 = __ldg(a.offsets + lo) + (rt - pre[lo]) * TOK;
+        it.rows = min(TOK, __ldg(a.offsets + lo + 1) - it.row0);
         return it;
     };
-    // 16-row weight blocks of a tile: SwiGLU takes two of the gate rows and two of the up rows
+    // block b (16 weight rows) of the first half of a tile: SwiGLU takes two of the gate rows and two
+    // of the up rows; the second half's blocks follow at a distance of 2 (SwiGLU) or 4 blocks
     auto block_of = [&](int tile, int b) {
-        return SWIGLU ? (b >> 1) * static_cast<int>(mblk / 2) + tile * 2 + (b & 1) : tile * 4 + b;
+        return SWIGLU ? (b >> 1) * static_cast<int>(mblk / 2) + tile * 2 * HALVES + (b & 1) : tile * 4 * HALVES + b;
     };
 
-    // ---- ring: the producer runs STAGES - 1 steps ahead of the consumer
-    const uint32_t ring = smem_u32(s_raw) + warp * STAGES * STAGE_BYTES;
+    // ---- ring: the producer runs STAGES - 1 stages ahead of the consumer
+    const uint32_t ring = smem_u32(s_raw) + warp * STAGES * STAGE_BYTES + lane * 16;
+    const uint32_t ring_sc = smem_u32(s_raw) + warp * STAGES * STAGE_BYTES + 2048 + t * 32 + g * 4;
+    const int64_t p_up = SWIGLU ? (mblk / 2) * blk_codes : 2 * blk_codes;
+    const int64_t half_codes = (SWIGLU ? 2 : 4) * blk_codes, half_scale = (SWIGLU ? 2 : 4) * blk_scale;
+    const int log_grp = a.group == 32 ? 5 : a.group == 64 ? 6 : 7;
     int64_t p_item = blockIdx.x;
-    int p_ks = nk, p_slot = 0;
+    int p_ks = nk;
+    uint32_t p_slot = 0;
     const uint8_t *p_codes = nullptr, *p_scale = nullptr;
-    int64_t p_up = 0;
-    auto produce = [&]() {
-        while (p_ks >= nk && p_item < total) {  // next item in which this warp's team has a tile
-            const Item it = locate(p_item);
-            p_item += gridDim.x;
-            if (it.tile >= tiles) continue;
-            p_ks = kw;
-            const int64_t first = it.e * mblk + block_of(it.tile, 0);
-            p_codes = a.codes + first * blk_codes + static_cast<int64_t>(kw) * 512 + lane * 16;
-            p_up = SWIGLU ? (mblk / 2) * blk_codes : 2 * blk_codes;
-            // lane (g, t) fetches block t's scales of rows g and g + 8
-            p_scale = a.scale + (it.e * mblk + block_of(it.tile, t)) * blk_scale + g * 4;
+    auto produce = [&](auto half) {
+        constexpr int H = decltype(half)::value;
+        if (H == 0) {
+            while (p_ks >= nk && p_item < total) {  // next item in which this warp's team has a tile
+                const Item it = locate(p_item);
+                p_item += gridDim.x;
+                if (it.tile >= tiles) continue;
+                p_ks = kw;
+                p_codes = a.codes + (it.e * mblk + block_of(it.tile, 0)) * blk_codes + kw * 512 + lane * 16;
+                // lane (g, t) fetches block t's scales of rows g and g + 8
+                p_scale = a.scale + (it.e * mblk + block_of(it.tile, t)) * blk_scale + g * 4;
+            }
         }
         if (p_ks < nk) {
-            const uint32_t dst = ring + p_slot * STAGE_BYTES;
-            cp_async16(dst + lane * 16, p_codes);
-            cp_async16(dst + 512 + lane * 16, p_codes + blk_codes);
-            cp_async16(dst + 1024 + lane * 16, p_codes + p_up);
-            cp_async16(dst + 1536 + lane * 16, p_codes + p_up + blk_codes);
-            const uint8_t* sc = p_scale + static_cast<int64_t>(p_ks * 64 / a.group) * 32;
-            cp_async4(dst + 2048 + t * 32 + g * 4, sc);
-            if (G32) cp_async4(dst + 2176 + t * 32 + g * 4, sc + 32);
-            p_codes += a.split * 512;
-            p_ks += a.split;
-            p_slot = p_slot + 1 == STAGES ? 0 : p_slot + 1;
+            const uint32_t dst = ring + p_slot;
+            const uint8_t* c = H ? p_codes + half_codes : p_codes;
+            const uint8_t* up = c + p_up;
+            cp_async16(dst, c);
+            cp_async16(dst + 512, c + blk_codes);
+            cp_async16(dst + 1024, up);
+            cp_async16(dst + 1536, up + blk_codes);
+            const uint8_t* sc = (H ? p_scale + half_scale : p_scale) + ((p_ks << 6 >> log_grp) << 5);
+            cp_async4(ring_sc + p_slot, sc);
+            if (G32) cp_async4(ring_sc + p_slot + 128, sc + 32);
+            if (H == HALVES - 1) {
+                p_codes += a.split * 512;
+                p_ks += a.split;
+            }
+            p_slot = p_slot == (STAGES - 1) * STAGE_BYTES ? 0u : p_slot + STAGE_BYTES;
         }
         cp_async_commit();
     };
-#pragma unroll
-    for (int i = 0; i < STAGES - 1; ++i) produce();
+    static_assert(STAGES == 4 && HALVES <= 2, "the halves alternate through the ring's prologue");
+    produce(Int<0>());
+    produce(Int<HALVES - 1>());
+    produce(Int<0>());
 
-    uint4 xn[2][2];
-    auto load_x = [&](const Item& it, int ks) {
-#pragma unroll
-        for (int n = 0; n < 2; ++n)
-#pragma unroll
-            for (int G = 0; G < 2; ++G)
-                xn[n][G] = g + 8 * n < it.rows
-                               ? __ldg(reinterpret_cast<const uint4*>(a.x + (it.row0 + g + 8 * n) * a.k + ks * 64 + 32 * G + 8 * t))
-                               : make_uint4(0, 0, 0, 0);
+    // ---- activations of the next step, in registers: rows g and g + 8 of the item. A row past the
+    // item's last repeats the last (its column of the product is not stored).
+    auto row_ptr = [&](const Item& it, int n) {
+        return a.x + static_cast<int64_t>(it.row0 + min(g + 8 * n, it.rows - 1)) * a.k + (kw * 64 + 8 * t);
+    };
+    auto load_x = [&](uint4 (&v)[MAXNT][2], const __nv_bfloat16* p, int64_t to_row8, int rows) {
+        v[0][0] = __ldg(reinterpret_cast<const uint4*>(p));
+        v[0][1] = __ldg(reinterpret_cast<const uint4*>(p + 32));
+        if (MAXNT > 1 && rows > 8) {
+            v[MAXNT - 1][0] = __ldg(reinterpret_cast<const uint4*>(p + to_row8));
+            v[MAXNT - 1][1] = __ldg(reinterpret_cast<const uint4*>(p + to_row8 + 32));
+        }
     };
     Item it{}, nx{};
+    const __nv_bfloat16 *xp = nullptr, *xnp = nullptr;
+    int64_t row8 = 0, row8n = 0;
+    uint4 xa[MAXNT][2], xb[MAXNT][2];
+#pragma unroll
+    for (int n = 0; n < MAXNT; ++n) xa[n][0] = xa[n][1] = xb[n][0] = xb[n][1] = make_uint4(0, 0, 0, 0);
     if (static_cast<int64_t>(blockIdx.x) < total) {
         nx = locate(blockIdx.x);
-        load_x(nx, kw);
+        xnp = row_ptr(nx, 0);
+        if (MAXNT > 1) row8n = row_ptr(nx, 1) - xnp;
+        load_x(xa, xnp, row8n, nx.rows);
     }
-    int slot = 0, buf = 0;
+    uint32_t slot = 0;
+    int buf = 0;
+    const uint8_t* my_ring = s_raw + warp * STAGES * STAGE_BYTES;
+    const int steps = (nk - kw + a.split - 1) / a.split;
+    const int x_step = a.split * 64;
     for (int64_t item = blockIdx.x; item < total; item += gridDim.x) {
         it = nx;
+        xp = xnp;
+        row8 = row8n;
         const bool more = item + gridDim.x < total;
-        if (more) nx = locate(item + gridDim.x);
+        if (more) {
+            nx = locate(item + gridDim.x);
+            xnp = row_ptr(nx, 0);
+            if (MAXNT > 1) row8n = row_ptr(nx, 1) - xnp;
+        }
         const bool mine = it.tile < tiles;
-        float acc[4][2][4];
+        float acc[4 * HALVES][MAXNT][4];
 #pragma unroll
-        for (int b = 0; b < 4; ++b)
+        for (int b = 0; b < 4 * HALVES; ++b)
 #pragma unroll
-            for (int n = 0; n < 2; ++n)
+            for (int n = 0; n < MAXNT; ++n)
 #pragma unroll
                 for (int i = 0; i < 4; ++i) acc[b][n][i] = 0.0f;
         if (mine) {
-            for (int ks = kw; ks < nk; ks += a.split) {
-                uint4 xv[2][2];
+            int left = steps;
+            // one step on the activations `v`, while those of the next step (of this item or the next) load into `w`
+            auto step = [&](auto nt, uint4 (&v)[MAXNT][2], uint4 (&w)[MAXNT][2]) {
+                constexpr int NT = decltype(nt)::value;
+                xp += x_step;
+                if (--left) load_x(w, xp, row8, it.rows);
+                else if (more) load_x(w, xnp, row8n, nx.rows);
+                auto half = [&](auto h, auto ahead) {
+                    cp_async_wait<STAGES - 2>();
+                    __syncwarp();  // the stage is visible, and the slot before it has been read by every lane
+                    produce(ahead);
+                    w4_stage<NT, MAXNT, G32>(my_ring + slot, lane, v, acc + 4 * decltype(h)::value);
+                    slot = slot == (STAGES - 1) * STAGE_BYTES ? 0u : slot + STAGE_BYTES;
+                };
+                half(Int<0>(), Int<HALVES - 1>());
+                if (HALVES > 1) half(Int<HALVES - 1>(), Int<0>());
+            };
+            auto run = [&](auto nt) {
+                while (true) {
+                    step(nt, xa, xb);
+                    if (!left) {
 #pragma unroll
-                for (int n = 0; n < 2; ++n)
-#pragma unroll
-                    for (int G = 0; G < 2; ++G) xv[n][G] = xn[n][G];
-                if (ks + a.split < nk) load_x(it, ks + a.split);
-                else if (more) load_x(nx, kw);
-                cp_async_wait<STAGES - 2>();
-                __syncwarp();  // the stage is visible, and the slot before it has been read by every lane
-                const uint8_t* stage = s_raw + (warp * STAGES + slot) * STAGE_BYTES;
-                produce();
-                if (it.rows > 8) w4_step<2, G32>(stage, lane, xv, acc);
-                else w4_step<1, G32>(stage, lane, xv, acc);
-                slot = slot + 1 == STAGES ? 0 : slot + 1;
-            }
+                        for (int n = 0; n < MAXNT; ++n) {
+                            xa[n][0] = xb[n][0];
+                            xa[n][1] = xb[n][1];
+                        }
+                        break;
+                    }
+                    step(nt, xb, xa);
+                    if (!left) break;
+                }
+            };
+            if (MAXNT > 1 && it.rows > 8) run(Int<MAXNT>());
+            else run(Int<1>());
         } else if (more) {
-            load_x(nx, kw);
+            load_x(xa, xnp, row8n, nx.rows);
         }
-        // join the team's partial sums, 8 rows at a time (two buffers: one barrier each)
-        const int parts = it.rows > 8 ? 2 : 1;
+        // join the team's partial sums, 8 rows x 64 weight rows at a time (two buffers: one barrier each)
 #pragma unroll
-        for (int n = 0; n < 2; ++n) {
-            if (n >= parts) break;
+        for (int ph = 0; ph < MAXNT * HALVES; ++ph) {
+            const int n = ph / HALVES, hf = ph % HALVES;
+            if (8 * n >= it.rows) break;
             float* r = red + buf * W4_WARPS * RED_WARP;
             float* w = r + warp * RED_WARP;
 #pragma unroll
             for (int b = 0; b < 4; ++b) {
-                w[(2 * t) * RED + 16 * b + g] = acc[b][n][0];
-                w[(2 * t + 1) * RED + 16 * b + g] = acc[b][n][1];
-                w[(2 * t) * RED + 16 * b + g + 8] = acc[b][n][2];
-                w[(2 * t + 1) * RED + 16 * b + g + 8] = acc[b][n][3];
+                w[(2 * t) * RED + 16 * b + g] = acc[4 * hf + b][n][0];
+                w[(2 * t + 1) * RED + 16 * b + g] = acc[4 * hf + b][n][1];
+                w[(2 * t) * RED + 16 * b + g + 8] = acc[4 * hf + b][n][2];
+                w[(2 * t + 1) * RED + 16 * b + g + 8] = acc[4 * hf + b][n][3];
             }
             __syncthreads();
             if (mine) {
@@ -374,7 +427,7 @@ __global__ void __launch_bounds__(W4_THREADS, 2) w4_kernel(const W4Args a) {
                             p += s[k * RED_WARP + row * RED + f];
                             if (SWIGLU) q += s[k * RED_WARP + row * RED + 32 + f];
                         }
-                        a.out[(it.row0 + 8 * n + row) * a.n_out + it.tile * FEAT + f] =
+                        a.out[static_cast<int64_t>(it.row0 + 8 * n + row) * a.n_out + (it.tile * HALVES + hf) * FEAT + f] =
                             __float2bfloat16_rn(SWIGLU ? silu_mul(p, q) : p);
                     }
                 }
@@ -385,27 +438,29 @@ __global__ void __launch_bounds__(W4_THREADS, 2) w4_kernel(const W4Args a) {
     cp_async_wait<0>();
 }
 
-template <bool SWIGLU, bool G32>
+template <bool SWIGLU, bool G32, int HALVES, int MAXNT>
 cudaError_t launch_w4_t(const W4Args& a, cudaStream_t st) {
     const DevInfo* di = current_device_info();
     if (!di) return cudaErrorUnknown;
     static PerDeviceOnce setup;
     const cudaError_t e = setup.run([](int) {
-        return cudaFuncSetAttribute(w4_kernel<SWIGLU, G32>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+        return cudaFuncSetAttribute(w4_kernel<SWIGLU, G32, HALVES, MAXNT>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                     static_cast<int>(RING_BYTES + RED_BYTES + 2049 * 4));
     });
     if (e != cudaSuccess) return e;
     const size_t smem = RING_BYTES + RED_BYTES + (static_cast<size_t>(a.N) + 1) * 4;
-    w4_kernel<SWIGLU, G32><<<di->sm_count * 2, W4_THREADS, smem, st>>>(a);
+    w4_kernel<SWIGLU, G32, HALVES, MAXNT><<<di->sm_count * 2, W4_THREADS, smem, st>>>(a);
     return cudaGetLastError();
 }
 
 template <bool SWIGLU>
-cudaError_t launch_w4(W4Args a, cudaStream_t st) {
+cudaError_t launch_w4(W4Args a, bool few_rows, cudaStream_t st) {
     // as many warps on a tile's reduction as leave each of them 8 steps of 64 columns
     a.split = W4_WARPS;
     while (a.split > 1 && a.k / 64 / a.split < 8) a.split /= 2;
-    return a.group == 32 ? launch_w4_t<SWIGLU, true>(a, st) : launch_w4_t<SWIGLU, false>(a, st);
+    if (few_rows && a.m % 128 == 0)
+        return a.group == 32 ? launch_w4_t<SWIGLU, true, 2, 1>(a, st) : launch_w4_t<SWIGLU, false, 2, 1>(a, st);
+    return a.group == 32 ? launch_w4_t<SWIGLU, true, 1, 2>(a, st) : launch_w4_t<SWIGLU, false, 1, 2>(a, st);
 }
 
 }  // namespace
@@ -429,7 +484,7 @@ cudaError_t launch_swiglu_w4(const void* x_perm, int64_t rows_cap, const int32_t
     W4Args a{offsets, static_cast<const __nv_bfloat16*>(x_perm), static_cast<const uint8_t*>(w13q),
              static_cast<const uint8_t*>(w13_scale), static_cast<__nv_bfloat16*>(h), status, rows_cap,
              N, d, 2 * I, I, group, 0};
-    return launch_w4<true>(a, st);
+    return launch_w4<true>(a, rows_cap < static_cast<int64_t>(8) * N, st);
 }
 
 cudaError_t launch_down_w4(const void* h, int64_t rows_cap, const int32_t* offsets, int N, const void* w2q,
@@ -438,7 +493,7 @@ cudaError_t launch_down_w4(const void* h, int64_t rows_cap, const int32_t* offse
     W4Args a{offsets, static_cast<const __nv_bfloat16*>(h), static_cast<const uint8_t*>(w2q),
              static_cast<const uint8_t*>(w2_scale), static_cast<__nv_bfloat16*>(y), status, rows_cap,
              N, I, d, d, group, 0};
-    return launch_w4<false>(a, st);
+    return launch_w4<false>(a, rows_cap < static_cast<int64_t>(8) * N, st);
 }
 
 }  // namespace lcmoe
