@@ -137,6 +137,9 @@ struct W4Args {
     int64_t rows_cap;
     int N, k, m, n_out, group;   // m: weight rows of an expert (2I or d)
     int split;                   // warps that share a tile's reduction (1, 2, 4 or 8)
+    // byte distances between 16-row blocks of the codes and of the scales: to the next block, and from
+    // a block of gate rows to the up rows of the same features (down product: two blocks on)
+    int64_t code_blk, scale_blk, code_up;
 };
 
 constexpr int W4_WARPS = 8;
@@ -239,8 +242,7 @@ __global__ void __launch_bounds__(W4_THREADS, 2) w4_kernel(const W4Args a) {
     const int team = warp / a.split, kw = warp % a.split;
     const int super = (tiles + teams - 1) / teams;  // items per row tile of an expert
     const int64_t total = static_cast<int64_t>(pre[a.N]) * super;
-    const int nk = a.k / 64, ngrp = a.k / a.group;
-    const int64_t blk_codes = static_cast<int64_t>(nk) * 512, blk_scale = static_cast<int64_t>(ngrp) * 32;
+    const int nk = a.k / 64;
     const int64_t mblk = a.m / 16;
 
     struct Item {
@@ -271,9 +273,7 @@ __global__ void __launch_bounds__(W4_THREADS, 2) w4_kernel(const W4Args a) {
     // ---- ring: the producer runs STAGES - 1 stages ahead of the consumer
     const uint32_t ring = smem_u32(s_raw) + warp * STAGES * STAGE_BYTES + lane * 16;
     const uint32_t ring_sc = smem_u32(s_raw) + warp * STAGES * STAGE_BYTES + 2048 + t * 32 + g * 4;
-    const int64_t p_up = SWIGLU ? (mblk / 2) * blk_codes : 2 * blk_codes;
-    const int64_t half_codes = (SWIGLU ? 2 : 4) * blk_codes, half_scale = (SWIGLU ? 2 : 4) * blk_scale;
-    const int log_grp = a.group == 32 ? 5 : a.group == 64 ? 6 : 7;
+    const uint32_t sc_step = 2048u / static_cast<uint32_t>(a.group);  // scale bytes per 64 columns
     int64_t p_item = blockIdx.x;
     int p_ks = nk;
     uint32_t p_slot = 0;
@@ -286,20 +286,20 @@ __global__ void __launch_bounds__(W4_THREADS, 2) w4_kernel(const W4Args a) {
                 p_item += gridDim.x;
                 if (it.tile >= tiles) continue;
                 p_ks = kw;
-                p_codes = a.codes + (it.e * mblk + block_of(it.tile, 0)) * blk_codes + kw * 512 + lane * 16;
+                p_codes = a.codes + (it.e * mblk + block_of(it.tile, 0)) * a.code_blk + kw * 512 + lane * 16;
                 // lane (g, t) fetches block t's scales of rows g and g + 8
-                p_scale = a.scale + (it.e * mblk + block_of(it.tile, t)) * blk_scale + g * 4;
+                p_scale = a.scale + (it.e * mblk + block_of(it.tile, t)) * a.scale_blk + g * 4;
             }
         }
         if (p_ks < nk) {
             const uint32_t dst = ring + p_slot;
-            const uint8_t* c = H ? p_codes + half_codes : p_codes;
-            const uint8_t* up = c + p_up;
+            const uint8_t* c = H ? p_codes + (SWIGLU ? 2 : 4) * a.code_blk : p_codes;
+            const uint8_t* up = c + a.code_up;
             cp_async16(dst, c);
-            cp_async16(dst + 512, c + blk_codes);
+            cp_async16(dst + 512, c + a.code_blk);
             cp_async16(dst + 1024, up);
-            cp_async16(dst + 1536, up + blk_codes);
-            const uint8_t* sc = (H ? p_scale + half_scale : p_scale) + ((p_ks << 6 >> log_grp) << 5);
+            cp_async16(dst + 1536, up + a.code_blk);
+            const uint8_t* sc = (H ? p_scale + (SWIGLU ? 2 : 4) * a.scale_blk : p_scale) + (p_ks * sc_step & ~31u);
             cp_async4(ring_sc + p_slot, sc);
             if (G32) cp_async4(ring_sc + p_slot + 128, sc + 32);
             if (H == HALVES - 1) {
@@ -456,6 +456,9 @@ cudaError_t launch_w4_t(const W4Args& a, cudaStream_t st) {
 template <bool SWIGLU>
 cudaError_t launch_w4(W4Args a, bool few_rows, cudaStream_t st) {
     // as many warps on a tile's reduction as leave each of them 8 steps of 64 columns
+    a.code_blk = static_cast<int64_t>(a.k / 64) * 512;
+    a.scale_blk = static_cast<int64_t>(a.k / a.group) * 32;
+    a.code_up = SWIGLU ? a.m / 32 * a.code_blk : 2 * a.code_blk;
     a.split = W4_WARPS;
     while (a.split > 1 && a.k / 64 / a.split < 8) a.split /= 2;
     if (few_rows && a.m % 128 == 0)
@@ -483,7 +486,7 @@ cudaError_t launch_swiglu_w4(const void* x_perm, int64_t rows_cap, const int32_t
                              cudaStream_t st) {
     W4Args a{offsets, static_cast<const __nv_bfloat16*>(x_perm), static_cast<const uint8_t*>(w13q),
              static_cast<const uint8_t*>(w13_scale), static_cast<__nv_bfloat16*>(h), status, rows_cap,
-             N, d, 2 * I, I, group, 0};
+             N, d, 2 * I, I, group, 0, 0, 0, 0};
     return launch_w4<true>(a, rows_cap < static_cast<int64_t>(8) * N, st);
 }
 
@@ -492,7 +495,7 @@ cudaError_t launch_down_w4(const void* h, int64_t rows_cap, const int32_t* offse
                            cudaStream_t st) {
     W4Args a{offsets, static_cast<const __nv_bfloat16*>(h), static_cast<const uint8_t*>(w2q),
              static_cast<const uint8_t*>(w2_scale), static_cast<__nv_bfloat16*>(y), status, rows_cap,
-             N, I, d, d, group, 0};
+             N, I, d, d, group, 0, 0, 0, 0};
     return launch_w4<false>(a, rows_cap < static_cast<int64_t>(8) * N, st);
 }
 
