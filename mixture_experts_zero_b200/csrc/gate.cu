@@ -16,7 +16,13 @@
 //                            D = sum_r ds_r s_r
 //
 // The picks are integers, so they are decided in 64 bits: two programs that evaluate the formula
-// in 64 bits agree on them unless two keys lie within about 1e-16 of each other.
+// in 64 bits agree on them unless two keys lie within about 1e-16 of each other. The kernel gets
+// there from fp32 keys with a bound on their error: it collects the keys within the bounds of the
+// K-th largest, sorts them, and evaluates them again in 64 bits where two neighbours in that order
+// are not apart by their bounds (a few tokens in a thousand).
+//
+// One warp per token, E / 32 logits a lane. What bounds it is instructions: per logit a load, an
+// exponential, a key and three comparisons, then about 300 a token for the choice.
 #include <cuda_bf16.h>
 
 #include "common.cuh"
@@ -80,114 +86,378 @@ __device__ __forceinline__ float chosen_share(float z, bool sigmoid) {
     return s / warp_sum(s);
 }
 
-// One warp per token; the token's keys lie in the warp's shared-memory row (doubles).
+__device__ __forceinline__ float redux_max(float v) {
+    float r;
+    asm("redux.sync.max.f32 %0, %1, 0xffffffff;" : "=f"(r) : "f"(v));
+    return r;
+}
+__device__ __forceinline__ float redux_min(float v) {
+    float r;
+    asm("redux.sync.min.f32 %0, %1, 0xffffffff;" : "=f"(r) : "f"(v));
+    return r;
+}
+
+// The 32 lanes' values in descending order over the lanes (bitonic network).
+__device__ __forceinline__ float sort_descending(float v) {
+    const int lane = threadIdx.x & 31;
+#pragma unroll
+    for (int k = 2; k <= 32; k *= 2)
+#pragma unroll
+        for (int j = k / 2; j; j /= 2) {
+            const float w = __shfl_xor_sync(FULL, v, j);
+            v = ((lane & j) == 0) == ((lane & k) == 0) ? fmaxf(v, w) : fminf(v, w);
+        }
+    return v;
+}
+
+// 64-bit softmax denominator of a row with maximum m (1 for a row of -inf, whose scores are 0).
 template <class LT>
+__device__ __noinline__ double softmax_sum64(const LT* zt, int E, float m) {
+    double part = 0.0;
+    for (int i = threadIdx.x & 31; i < E; i += 32) {
+        const float z = load_logit(zt + i);
+        part += z == m && m < 0.0f && isinf(m) ? 0.0 : exp(static_cast<double>(z) - m);
+    }
+    const double S = warp_sum(part);
+    return S == 0.0 ? 1.0 : S;
+}
+
+__device__ __forceinline__ double score64(float z, float m, double S, bool sigmoid) {
+    if (sigmoid) return sigmoid64(z);
+    return z == m && m < 0.0f && isinf(m) ? 0.0 : exp(static_cast<double>(z) - m) / S;
+}
+
+// The whole choice in 64 bits, for any row (K rounds of a warp-wide maximum over the keys, which
+// lie in the warp's shared-memory row): lane r < K returns its pick, or -1 in every lane where a key
+// or a group's score is NaN.
+template <class LT>
+__device__ __noinline__ int pick64(const LT* zt, const float* bias, int E, int K, const lc_moe_gate_opts& o,
+                                   float m, double* key) {
+    const int lane = threadIdx.x & 31;
+    const bool sigmoid = o.score == LC_MOE_SCORE_SIGMOID;
+    const double S = sigmoid ? 1.0 : softmax_sum64(zt, E, m);
+    const int size = E / o.groups;
+    bool nan = false;
+    __syncwarp();
+    for (int i = lane; i < E; i += 32) {
+        const double s = score64(load_logit(zt + i), m, S, sigmoid);
+        const double k = bias ? s + static_cast<double>(__ldg(bias + i)) : s;
+        nan |= k != k;
+        key[i] = k;
+    }
+    __syncwarp();
+    uint32_t kept = FULL;  // bit g: group g stays
+    if (o.top_groups < o.groups) {
+        unsigned long long mine = 0;  // lane g: the ordered score of group g
+        for (int g = 0; g < o.groups; ++g) {
+            double a = -INFINITY, b = -INFINITY;
+            for (int i = lane; i < size; i += 32) {
+                const double k = key[g * size + i];
+                if (k > a) { b = a; a = k; }
+                else if (k > b) b = k;
+            }
+#pragma unroll
+            for (int w = 16; w; w >>= 1) {
+                const double a2 = __shfl_xor_sync(FULL, a, w), b2 = __shfl_xor_sync(FULL, b, w);
+                b = fmax(fmin(a, a2), fmax(b, b2));
+                a = fmax(a, a2);
+            }
+            const double score = o.group_rank == 2 && size > 1 ? a + b : a;
+            nan |= score != score;
+            if (lane == g) mine = ordered(score);
+        }
+        kept = 0;
+        for (int r = 0; r < o.top_groups; ++r) {
+            const int g = arg_max(mine, lane);
+            kept |= 1u << g;
+            if (lane == g) mine = 0;
+        }
+    }
+    if (__any_sync(FULL, nan)) return -1;
+    unsigned long long taken = 0, best = 0;
+    int at = 0x7fffffff, my_idx = 0;
+    auto offer = [&]() {  // this lane's best untaken key
+        best = 0;
+        at = 0x7fffffff;
+        for (int i = lane, j = 0; i < E; i += 32, ++j) {
+            if ((taken >> j) & 1) continue;
+            if (o.top_groups < o.groups && !((kept >> (i / size)) & 1u)) continue;
+            const unsigned long long k = ordered(key[i]);
+            if (k > best) {
+                best = k;
+                at = i;
+            }
+        }
+    };
+    offer();
+    for (int r = 0; r < K; ++r) {
+        const int w = arg_max(best, at);
+        if (lane == r) my_idx = w;
+        if ((w & 31) == lane) {
+            taken |= 1ull << (w >> 5);
+            offer();
+        }
+    }
+    return my_idx;
+}
+
+// Error bounds of the fp32 keys. u = 2^-23.
+//   softmax: __expf is within 2 + 1.2 x steps at -x = z - m, whose rounding adds x / 2; the sum of E
+//   terms averages that over the softmax (x is ln E <= 7.7 on average at most: 15 steps), its 29
+//   additions in sequence add 15, quotient, product and sum 2: s is within (36 + 1.7 x) u s, which
+//   is at most 36 u / S for any x >= 0, and 2^-15 s for every x <= 88.
+//   sigmoid: (6 + 1.2 max(-z, 0)) u s, at most 7 u for any z, and 2^-16 s for every z >= -88.
+//   Scores below e^-87 count as 0 (1e-37 covers them); key = s + b adds u |key|.
+constexpr float U23 = 1.1920929e-07f;
+
+template <class LT, int VPL>
 __global__ void __launch_bounds__(GATE_THREADS)
     gate_kernel(const LT* __restrict__ logits, const float* __restrict__ bias, int T, int E, int K,
                 lc_moe_gate_opts o, int32_t* __restrict__ idx, float* __restrict__ gate,
                 int32_t* __restrict__ counts, uint32_t* __restrict__ status) {
     extern __shared__ double s_dyn[];
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, warps = blockDim.x >> 5;
-    double* key = s_dyn + static_cast<size_t>(warp) * E;
-    int32_t* s_hist = reinterpret_cast<int32_t*>(s_dyn + static_cast<size_t>(warps) * E);
+    double* row64 = s_dyn + static_cast<size_t>(warp) * max(E, 32);  // this warp's keys, or its candidates
+    float* row32 = reinterpret_cast<float*>(row64);
+    int32_t* cand = reinterpret_cast<int32_t*>(row64);
+    int32_t* s_hist = reinterpret_cast<int32_t*>(s_dyn + static_cast<size_t>(warps) * max(E, 32));
     if (counts) {
         for (int i = threadIdx.x; i < E; i += blockDim.x) s_hist[i] = 0;
         __syncthreads();
     }
+    const float NEG_INF = __int_as_float(0xff800000);
     const bool sigmoid = o.score == LC_MOE_SCORE_SIGMOID;
+    const bool grouped = o.top_groups < o.groups;
+    // without a bias and without sums of scores the logits themselves are in the keys' order
+    const bool by_z = !bias && (!grouped || o.group_rank == 1);
     const int size = E / o.groups;
-    for (int t = blockIdx.x * warps + warp; t < T; t += gridDim.x * warps) {
-        const LT* zt = logits + static_cast<int64_t>(t) * E;
-        __syncwarp();
-        float m = __int_as_float(0xff800000);
-        double S = 1.0;
-        if (!sigmoid) {
-            for (int i = lane; i < E; i += 32) m = fmaxf(m, load_logit(zt + i));
-            m = warp_max(m);
-            double part = 0.0;
-            for (int i = lane; i < E; i += 32) {
-                const float z = load_logit(zt + i);
-                part += z == m && m < 0.0f && isinf(m) ? 0.0 : exp(static_cast<double>(z) - m);
-            }
-            S = warp_sum(part);
-            if (S == 0.0) S = 1.0;  // every logit is -inf: all scores are 0
-        }
-        bool nan = false;
+    float bmin = 0.0f;  // the smallest finite bias: score = key - b <= key - bmin
+    if (bias) {
+        bmin = __int_as_float(0x7f800000);
         for (int i = lane; i < E; i += 32) {
-            const float z = load_logit(zt + i);
-            double s;
-            if (sigmoid) s = sigmoid64(z);
-            else s = (z == m && m < 0.0f && isinf(m)) ? 0.0 : exp(static_cast<double>(z) - m) / S;
-            const double k = bias ? s + static_cast<double>(bias[i]) : s;
-            nan |= k != k;
-            key[i] = k;
+            const float b = __ldg(bias + i);
+            if (b > NEG_INF) bmin = fminf(bmin, b);
+        }
+        bmin = redux_min(bmin);
+    }
+    constexpr bool PREFETCH = VPL <= 32;
+    float vn[PREFETCH ? VPL : 1];
+    auto load = [&](int tt, float* dst) {
+        const LT* z = logits + static_cast<int64_t>(tt) * E;
+#pragma unroll
+        for (int j = 0; j < VPL; ++j) {
+            const int i = lane + 32 * j;
+            dst[j] = (tt < T && i < E) ? load_logit(z + i) : NEG_INF;
+        }
+    };
+    const int stride = gridDim.x * warps;
+    if (PREFETCH) load(blockIdx.x * warps + warp, vn);
+    for (int t = blockIdx.x * warps + warp; t < T; t += stride) {
+        const LT* zt = logits + static_cast<int64_t>(t) * E;
+        float v[VPL];
+        if (PREFETCH) {
+#pragma unroll
+            for (int j = 0; j < VPL; ++j) v[j] = vn[PREFETCH ? j : 0];
+            load(t + stride, vn);
+        } else {
+            load(t, v);
+        }
+        float m = NEG_INF, S = 1.0f, inv_S = 1.0f;
+        bool nan = false;
+        if (!sigmoid) {
+#pragma unroll
+            for (int j = 0; j < VPL; ++j) m = fmaxf(m, v[j]);
+            m = redux_max(m);
+        }
+        const float m0 = m == NEG_INF ? 0.0f : m;
+        if (by_z) {
+#pragma unroll
+            for (int j = 0; j < VPL; ++j) nan |= v[j] != v[j];
+            nan |= !sigmoid && m == __int_as_float(0x7f800000);
+            if (!sigmoid && !o.renorm) {
+                float part = 0.0f;
+#pragma unroll
+                for (int j = 0; j < VPL; ++j) part += __expf(v[j] - m0);
+                S = warp_sum(part);
+                inv_S = S > 0.0f ? 1.0f / S : 0.0f;
+            }
+        } else {
+            if (sigmoid) {
+#pragma unroll
+                for (int j = 0; j < VPL; ++j) v[j] = __fdividef(1.0f, 1.0f + __expf(-v[j]));
+            } else {
+                float part = 0.0f;
+#pragma unroll
+                for (int j = 0; j < VPL; ++j) {
+                    v[j] = __expf(v[j] - m0);
+                    part += v[j];
+                }
+                S = warp_sum(part);
+                inv_S = S > 0.0f || S != S ? 1.0f / S : 0.0f;
+            }
+#pragma unroll
+            for (int j = 0; j < VPL; ++j) {
+                const int i = lane + 32 * j;
+                const float b = bias && i < E ? __ldg(bias + i) : 0.0f;
+                v[j] = i < E ? fmaf(v[j], inv_S, b) : NEG_INF;
+                nan |= v[j] != v[j];
+            }
+        }
+        // bound on the error of a key k whose score is at most top
+        auto error_of = [&](float k) {
+            if (by_z) {
+                // logits are exact; where the 64-bit score hardly depends on them they decide nothing
+                if (sigmoid ? k < -700.0f : m0 - k > 700.0f) return __int_as_float(0x7f800000);
+                return 1e-13f + (sigmoid ? 1e-15f * __expf(fminf(k, 80.0f)) : 0.0f);
+            }
+            const float rel = (sigmoid ? 0x1p-16f : 0x1p-15f) * (k - bmin), all = (sigmoid ? 7.0f : 36.0f * inv_S) * U23;
+            return fminf(rel, all) + U23 * fabsf(k) + 1e-37f;
+        };
+        bool sure = !__any_sync(FULL, nan);
+        if (grouped && sure) {
+            // group scores: teams of lanes over the keys in shared memory
+            __syncwarp();
+#pragma unroll
+            for (int j = 0; j < VPL; ++j)
+                if (lane + 32 * j < E) row32[lane + 32 * j] = v[j];
+            __syncwarp();
+            int team = 32;  // lanes to a group: a power of two, so that all groups run at once
+            while (team * o.groups > 32) team >>= 1;
+            const int g = lane / team, part = lane % team;
+            float a = NEG_INF, b = NEG_INF;
+            if (g < o.groups)
+                for (int i = part; i < size; i += team) {
+                    const float k = row32[g * size + i];
+                    b = fmaxf(b, fminf(a, k));
+                    a = fmaxf(a, k);
+                }
+            for (int w = 1; w < team; w <<= 1) {
+                const float a2 = __shfl_xor_sync(FULL, a, w), b2 = __shfl_xor_sync(FULL, b, w);
+                b = fmaxf(fminf(a, a2), fmaxf(b, b2));
+                a = fmaxf(a, a2);
+            }
+            const bool two = o.group_rank == 2 && size > 1;
+            float score = two ? a + b : a;
+            float err = two ? error_of(a) + error_of(b) + U23 * fabsf(score) : error_of(a);
+            // lane g: group g
+            score = __shfl_sync(FULL, score, (lane * team) & 31);
+            err = __shfl_sync(FULL, err, (lane * team) & 31);
+            if (lane >= o.groups) score = NEG_INF;
+            int rank = 0;
+            for (int q = 0; q < o.groups; ++q) {
+                const float other = __shfl_sync(FULL, score, q);
+                rank += other > score || (other == score && q < lane);
+            }
+            const uint32_t kept = __ballot_sync(FULL, lane < o.groups && rank < o.top_groups);
+            // the groups that stay and those that leave are apart by their bounds (infinite scores have no
+            // bound and are what they are in 64 bits)
+            const float low = redux_min(((kept >> lane) & 1u) ? score - err : __int_as_float(0x7f800000));
+            const float high = redux_max(lane < o.groups && !((kept >> lane) & 1u) ? score + err : NEG_INF);
+            sure = low > high && !__any_sync(FULL, score != score);
+#pragma unroll
+            for (int j = 0; j < VPL; ++j) {
+                const int i = lane + 32 * j;
+                if (i < E && !((kept >> (i / size)) & 1u)) v[j] = NEG_INF;
+            }
+        }
+        int total = 0;
+        if (sure) {
+            // the K-th largest of the lanes' largest keys is at most the K-th largest key
+            float top = NEG_INF;
+#pragma unroll
+            for (int j = 0; j < VPL; ++j) top = fmaxf(top, v[j]);
+            const float tau = __shfl_sync(FULL, sort_descending(top), K - 1);
+            const float least = tau - 2.0f * error_of(tau) - U23 * fabsf(tau);
+            if (least > NEG_INF) {
+                int mine = 0;
+#pragma unroll
+                for (int j = 0; j < VPL; ++j) mine += v[j] >= least;
+                int before = mine;
+#pragma unroll
+                for (int w = 1; w < 32; w <<= 1) {
+                    const int n = __shfl_up_sync(FULL, before, w);
+                    if (lane >= w) before += n;
+                }
+                total = __shfl_sync(FULL, before, 31);
+                __syncwarp();
+                if (total <= 32 && mine) {
+                    before -= mine;
+#pragma unroll
+                    for (int j = 0; j < VPL; ++j)
+                        if (v[j] >= least) cand[before++] = lane + 32 * j;
+                }
+            }
+        }
+        int my_idx;
+        float z = NEG_INF;
+        if (total && total <= 32) {
+            __syncwarp();
+            // one candidate a lane: key and bound again, then its rank among them
+            int i = lane < total ? cand[lane] : 0x7fffffff;
+            float k = NEG_INF, err = 0.0f, b = 0.0f;
+            if (lane < total) {
+                z = load_logit(zt + i);
+                b = bias ? __ldg(bias + i) : 0.0f;
+                if (by_z) {
+                    k = z;
+                    err = error_of(z);
+                } else if (sigmoid) {
+                    const float s = __fdividef(1.0f, 1.0f + __expf(-z));
+                    k = s + b;
+                    err = s * (6.0f + 1.2f * fminf(fmaxf(-z, 0.0f), 88.0f)) * U23 + U23 * fabsf(k) + 1e-37f;
+                } else {
+                    const float s = __expf(z - m0) * inv_S;
+                    k = s + b;
+                    err = s * (36.0f + 1.7f * fminf(m0 - z, 88.0f)) * U23 + U23 * fabsf(k) + 1e-37f;
+                }
+            }
+            int rank = 0;
+            for (int q = 0; q < total; ++q) {
+                const float kq = __shfl_sync(FULL, k, q);
+                const int iq = __shfl_sync(FULL, i, q);
+                rank += kq > k || (kq == k && iq < i);
+            }
+            // neighbours in the order: apart by their bounds, or equal in logit and bias
+            __syncwarp();
+            if (lane < total) cand[rank] = lane;
+            __syncwarp();
+            const int from = lane < total ? cand[lane] : lane;
+            const int i_s = __shfl_sync(FULL, i, from);
+            const float k_s = __shfl_sync(FULL, k, from), e_s = __shfl_sync(FULL, err, from);
+            const float z_s = __shfl_sync(FULL, z, from), b_s = __shfl_sync(FULL, b, from);
+            const float k_n = __shfl_down_sync(FULL, k_s, 1), e_n = __shfl_down_sync(FULL, e_s, 1);
+            const float z_n = __shfl_down_sync(FULL, z_s, 1), b_n = __shfl_down_sync(FULL, b_s, 1);
+            const bool close = lane < K && lane + 1 < total && !(k_s - k_n > e_s + e_n) && !(z_s == z_n && b_s == b_n);
+            my_idx = i_s;
+            if (__any_sync(FULL, close)) {
+                const double S64 = sigmoid ? 1.0 : softmax_sum64(zt, E, m);
+                const double k64 = lane < total ? score64(z, m, S64, sigmoid) + static_cast<double>(b) : -INFINITY;
+                rank = 0;
+                for (int q = 0; q < total; ++q) {
+                    const double kq = __shfl_sync(FULL, k64, q);
+                    const int iq = __shfl_sync(FULL, i, q);
+                    rank += kq > k64 || (kq == k64 && iq < i);
+                }
+                __syncwarp();
+                if (lane < total) cand[rank] = i;
+                __syncwarp();
+                my_idx = lane < total ? cand[lane] : 0;
+            }
+        } else {
+            my_idx = pick64(zt, bias, E, K, o, m, row64);
         }
         __syncwarp();
-        uint32_t kept = FULL;  // bit g: group g stays
-        if (o.top_groups < o.groups) {
-            unsigned long long mine = 0;  // lane g: the ordered score of group g
-            for (int g = 0; g < o.groups; ++g) {
-                double a = -INFINITY, b = -INFINITY;
-                for (int i = lane; i < size; i += 32) {
-                    const double k = key[g * size + i];
-                    if (k > a) { b = a; a = k; }
-                    else if (k > b) b = k;
-                }
-#pragma unroll
-                for (int w = 16; w; w >>= 1) {
-                    const double a2 = __shfl_xor_sync(FULL, a, w), b2 = __shfl_xor_sync(FULL, b, w);
-                    b = fmax(fmin(a, a2), fmax(b, b2));
-                    a = fmax(a, a2);
-                }
-                const double score = o.group_rank == 2 && size > 1 ? a + b : a;
-                nan |= score != score;
-                if (lane == g) mine = ordered(score);
-            }
-            kept = 0;
-            for (int r = 0; r < o.top_groups; ++r) {
-                const int g = arg_max(mine, lane);
-                kept |= 1u << g;
-                if (lane == g) mine = 0;
-            }
-        }
-        int my_idx = 0;
-        const bool bad = __any_sync(FULL, nan);
+        const bool bad = my_idx < 0;  // in every lane
         if (bad) {
             my_idx = lane;
             if (lane == 0) set_status(status, LC_MOE_DEV_NAN_KEY);
-        } else {
-            // K rounds of warp arg-max; each lane offers its best untaken key
-            unsigned long long taken = 0, best = 0;
-            int at = 0x7fffffff;
-            auto offer = [&]() {
-                best = 0;
-                at = 0x7fffffff;
-                for (int i = lane, j = 0; i < E; i += 32, ++j) {
-                    if ((taken >> j) & 1) continue;
-                    if (!((kept >> (i / size)) & 1u) && o.top_groups < o.groups) continue;
-                    const unsigned long long k = ordered(key[i]);
-                    if (k > best) {
-                        best = k;
-                        at = i;
-                    }
-                }
-            };
-            offer();
-            for (int r = 0; r < K; ++r) {
-                const int w = arg_max(best, at);
-                if (lane == r) my_idx = w;
-                if ((w & 31) == lane) {
-                    taken |= 1ull << (w >> 5);
-                    offer();
-                }
-            }
         }
         // gates, from the chosen logits
-        const float z = lane < K ? load_logit(zt + my_idx) : __int_as_float(0xff800000);
+        z = lane < K ? load_logit(zt + my_idx) : NEG_INF;
         float g;
         if (o.renorm) g = chosen_share(z, sigmoid);
         else if (sigmoid) g = sigmoid32(z);
-        else g = static_cast<float>(isinf(z) ? 0.0 : exp(static_cast<double>(z) - m) / S);
+        else g = expf(z - m0) * inv_S;
         if (lane < K) {
             const int64_t at = static_cast<int64_t>(t) * K + lane;
             idx[at] = my_idx;
@@ -273,30 +543,51 @@ __global__ void __launch_bounds__(GATE_THREADS)
 
 }  // namespace
 
+namespace {
+
+template <class LT, int VPL>
+cudaError_t launch_gate_t(const LT* logits, const float* bias, int T, int E, int K, const lc_moe_gate_opts& o,
+                          int32_t* idx, float* gate, int32_t* counts, uint32_t* status, cudaStream_t st) {
+    const DevInfo* di = current_device_info();
+    if (!di) return cudaErrorUnknown;
+    constexpr int MAX_WARPS = VPL <= 32 ? 8 : 4;
+    constexpr int MAX_SMEM = MAX_WARPS * 32 * VPL * 8 + 32 * VPL * 4;
+    static PerDeviceOnce setup;
+    const cudaError_t e = setup.run([](int) {
+        return cudaFuncSetAttribute(gate_kernel<LT, VPL>, cudaFuncAttributeMaxDynamicSharedMemorySize, MAX_SMEM);
+    });
+    if (e != cudaSuccess) return e;
+    // few tokens: spread them over the SMs
+    const int warps = T <= di->sm_count ? 1 : T <= 4 * di->sm_count ? 2 : MAX_WARPS;
+    const size_t smem = static_cast<size_t>(warps) * (E > 32 ? E : 32) * 8 + (counts ? static_cast<size_t>(E) * 4 : 0);
+    int blocks = (T + warps - 1) / warps;
+    if (blocks > di->sm_count * 4) blocks = di->sm_count * 4;
+    gate_kernel<LT, VPL><<<blocks, warps * 32, smem, st>>>(logits, bias, T, E, K, o, idx, gate, counts, status);
+    return cudaGetLastError();
+}
+
+template <class LT>
+cudaError_t launch_gate_l(const LT* logits, const float* bias, int T, int E, int K, const lc_moe_gate_opts& o,
+                          int32_t* idx, float* gate, int32_t* counts, uint32_t* status, cudaStream_t st) {
+    const int vpl = (E + 31) / 32;
+    if (vpl <= 1) return launch_gate_t<LT, 1>(logits, bias, T, E, K, o, idx, gate, counts, status, st);
+    if (vpl <= 4) return launch_gate_t<LT, 4>(logits, bias, T, E, K, o, idx, gate, counts, status, st);
+    if (vpl <= 8) return launch_gate_t<LT, 8>(logits, bias, T, E, K, o, idx, gate, counts, status, st);
+    if (vpl <= 12) return launch_gate_t<LT, 12>(logits, bias, T, E, K, o, idx, gate, counts, status, st);
+    if (vpl <= 16) return launch_gate_t<LT, 16>(logits, bias, T, E, K, o, idx, gate, counts, status, st);
+    if (vpl <= 24) return launch_gate_t<LT, 24>(logits, bias, T, E, K, o, idx, gate, counts, status, st);
+    if (vpl <= 32) return launch_gate_t<LT, 32>(logits, bias, T, E, K, o, idx, gate, counts, status, st);
+    return launch_gate_t<LT, 64>(logits, bias, T, E, K, o, idx, gate, counts, status, st);
+}
+
+}  // namespace
+
 cudaError_t launch_gate(const void* logits, int bf16, const float* bias, int T, int E, int K,
                         const lc_moe_gate_opts& o, int32_t* idx, float* gate, int32_t* counts,
                         uint32_t* status, cudaStream_t st) {
-    const DevInfo* di = current_device_info();
-    if (!di) return cudaErrorUnknown;
-    const int warps = E <= 1024 ? 8 : 4;
-    const size_t smem = static_cast<size_t>(warps) * E * 8 + (counts ? static_cast<size_t>(E) * 4 : 0);
-    static PerDeviceOnce setup;
-    const cudaError_t e = setup.run([](int) {
-        cudaError_t r = cudaFuncSetAttribute(gate_kernel<float>, cudaFuncAttributeMaxDynamicSharedMemorySize, 80 * 1024);
-        if (r == cudaSuccess)
-            r = cudaFuncSetAttribute(gate_kernel<__nv_bfloat16>, cudaFuncAttributeMaxDynamicSharedMemorySize, 80 * 1024);
-        return r;
-    });
-    if (e != cudaSuccess) return e;
-    int blocks = (T + warps - 1) / warps;
-    if (blocks > di->sm_count * 4) blocks = di->sm_count * 4;
     if (bf16)
-        gate_kernel<__nv_bfloat16><<<blocks, warps * 32, smem, st>>>(
-            static_cast<const __nv_bfloat16*>(logits), bias, T, E, K, o, idx, gate, counts, status);
-    else
-        gate_kernel<float><<<blocks, warps * 32, smem, st>>>(static_cast<const float*>(logits), bias, T, E, K, o,
-                                                              idx, gate, counts, status);
-    return cudaGetLastError();
+        return launch_gate_l(static_cast<const __nv_bfloat16*>(logits), bias, T, E, K, o, idx, gate, counts, status, st);
+    return launch_gate_l(static_cast<const float*>(logits), bias, T, E, K, o, idx, gate, counts, status, st);
 }
 
 cudaError_t launch_gate_backward(const void* logits, int bf16, const int32_t* idx, const float* dgate, int T,
