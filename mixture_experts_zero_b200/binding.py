@@ -132,6 +132,18 @@ def _stream(stream) -> ctypes.c_void_p:
     return ctypes.c_void_p(stream.cuda_stream)
 
 
+# The handle of the current stream without building a Stream object (0.1 instead of 3.1 us a call).
+_RAW_STREAM = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+
+
+def _raw_stream(stream, device) -> int:
+    if stream is not None:
+        return stream.cuda_stream
+    if _RAW_STREAM is not None:
+        return _RAW_STREAM(device.index)
+    return torch.cuda.current_stream(device).cuda_stream
+
+
 def _need(t: torch.Tensor, dtype, shape, name):
     if t.dtype != dtype:
         raise TypeError(f"{name}: expected {dtype}, got {t.dtype}")
@@ -540,6 +552,32 @@ def _one_device(**tensors):
             raise ValueError(f"{name}: on {t.device}, but the current device is cuda:{cur}")
 
 
+def _device_of(t, name):
+    """The device of a call's first tensor: the current CUDA device, or an error."""
+    d = t.device
+    if d.type != "cuda" or d.index != torch.cuda.current_device():
+        _one_device(**{name: t})
+    return d
+
+
+def _expect(t, dtype, shape, device, name):
+    """t: a contiguous tensor of that type, shape and device (one test of four where it is right)."""
+    if t.dtype is dtype and t.device == device and t.shape == shape and t.is_contiguous():
+        return
+    _need(t, dtype, shape, name)
+    _one_device(**{name: t})
+
+
+def _expect_ws(ws, device):
+    if ws.device != device or not ws.is_contiguous():
+        _one_device(ws=ws)
+        raise ValueError(f"ws: on {ws.device}, expected {device}")
+
+
+def _addr(t):
+    return None if t is None else t.data_ptr()
+
+
 def _alloc_on(stream):
     """Buffers that a call makes itself belong to the stream it runs on."""
     return contextlib.nullcontext() if stream is None else torch.cuda.stream(stream)
@@ -564,26 +602,31 @@ def lc_moe_gate(logits, bias, K: int, N: int, score: str = "softmax", groups: in
     fp32 [E] or None, the ``top_groups`` best of ``groups`` groups of experts (by the sum of their
     ``group_rank`` largest keys), gates renormalised or not, times ``scale``. Returns (idx, gate)."""
     T, E = _dims_of(logits, 2, "logits")
-    if logits.dtype not in LOGITS_TYPES:
+    kind = LOGITS_TYPES.get(logits.dtype)
+    if kind is None:
         raise TypeError(f"logits: expected float32 or bfloat16, got {logits.dtype}")
-    _one_device(logits=logits, bias=bias, idx=idx, gate=gate, counts=counts, ws=ws)
+    dev = _device_of(logits, "logits")
+    _expect(logits, logits.dtype, (T, E), dev, "logits")
     o = _gate_opts(score, groups, top_groups, group_rank, renorm, scale)
     if bias is not None:
-        _need(bias, torch.float32, (E,), "bias")
+        _expect(bias, torch.float32, (E,), dev, "bias")
+    if counts is not None:
+        _expect(counts, torch.int32, (E,), dev, "counts")
+    if idx is not None:
+        _expect(idx, torch.int32, (T, K), dev, "idx")
+    if gate is not None:
+        _expect(gate, torch.float32, (T, K), dev, "gate")
     with _alloc_on(stream):
         if idx is None:
-            idx = torch.empty(T, K, dtype=torch.int32, device=logits.device)
+            idx = torch.empty(T, K, dtype=torch.int32, device=dev)
         if gate is None:
-            gate = torch.empty(T, K, dtype=torch.float32, device=logits.device)
+            gate = torch.empty(T, K, dtype=torch.float32, device=dev)
         if ws is None:
-            ws = _status_ws(logits.device)
-    _need(idx, torch.int32, (T, K), "idx")
-    _need(gate, torch.float32, (T, K), "gate")
-    if counts is not None:
-        _need(counts, torch.int32, (E,), "counts")
+            ws = _status_ws(dev)
+    _expect_ws(ws, dev)
     s = Shape(T, 64, N, E - N, K, 64)
-    _check(_lib().lc_moe_gate(ctypes.byref(s), ctypes.byref(o), _ptr(logits), LOGITS_TYPES[logits.dtype], _ptr(bias),
-                              _ptr(idx), _ptr(gate), _ptr(counts), _ptr(ws), ws.numel(), _stream(stream)),
+    _check(_lib().lc_moe_gate(ctypes.byref(s), ctypes.byref(o), logits.data_ptr(), kind, _addr(bias), idx.data_ptr(),
+                              gate.data_ptr(), _addr(counts), ws.data_ptr(), ws.nbytes, _raw_stream(stream, dev)),
            "lc_moe_gate")
     return idx, gate
 
@@ -593,22 +636,26 @@ def lc_moe_gate_backward(logits, idx, dgate, score: str = "softmax", renorm: boo
     """Gradient of lc_moe_gate's gates for the logits, the picks ``idx`` held fixed."""
     T, E = _dims_of(logits, 2, "logits")
     K = _dims_of(idx, 2, "idx")[1]
-    if logits.dtype not in LOGITS_TYPES:
+    kind = LOGITS_TYPES.get(logits.dtype)
+    if kind is None:
         raise TypeError(f"logits: expected float32 or bfloat16, got {logits.dtype}")
-    _one_device(logits=logits, idx=idx, dgate=dgate, dlogits=dlogits, ws=ws)
+    dev = _device_of(logits, "logits")
+    _expect(logits, logits.dtype, (T, E), dev, "logits")
     o = _gate_opts(score, 1, 1, 1, renorm, scale)
-    _need(idx, torch.int32, (T, K), "idx")
-    _need(dgate, torch.float32, (T, K), "dgate")
+    _expect(idx, torch.int32, (T, K), dev, "idx")
+    _expect(dgate, torch.float32, (T, K), dev, "dgate")
+    if dlogits is not None:
+        _expect(dlogits, logits.dtype, (T, E), dev, "dlogits")
     with _alloc_on(stream):
         if dlogits is None:
-            dlogits = torch.empty_like(logits)
+            dlogits = torch.empty(T, E, dtype=logits.dtype, device=dev)
         if ws is None:
-            ws = _status_ws(logits.device)
-    _need(dlogits, logits.dtype, (T, E), "dlogits")
+            ws = _status_ws(dev)
+    _expect_ws(ws, dev)
     s = Shape(T, 64, E, 0, K, 64)
-    _check(_lib().lc_moe_gate_backward(ctypes.byref(s), ctypes.byref(o), _ptr(logits), LOGITS_TYPES[logits.dtype],
-                                       _ptr(idx), _ptr(dgate), _ptr(dlogits), _ptr(ws), ws.numel(), _stream(stream)),
-           "lc_moe_gate_backward")
+    _check(_lib().lc_moe_gate_backward(ctypes.byref(s), ctypes.byref(o), logits.data_ptr(), kind, idx.data_ptr(),
+                                       dgate.data_ptr(), dlogits.data_ptr(), ws.data_ptr(), ws.nbytes,
+                                       _raw_stream(stream, dev)), "lc_moe_gate_backward")
     return dlogits
 
 
@@ -619,28 +666,33 @@ def lc_moe_combine_backward(dout, x, y, gate, pair_row, dy=None, dgate=None, dx=
     T, d = _dims_of(dout, 2, "dout")
     K = _dims_of(gate, 2, "gate")[1]
     rows = _dims_of(y, 2, "y")[0]
-    _one_device(dout=dout, x=x, y=y, gate=gate, pair_row=pair_row, dy=dy, dgate=dgate, dx=dx, ws=ws)
-    _need(dout, torch.bfloat16, (T, d), "dout")
-    _need(x, torch.bfloat16, (T, d), "x")
-    _need(y, torch.bfloat16, (rows, d), "y")
-    _need(gate, torch.float32, (T, K), "gate")
-    _need(pair_row, torch.int32, (T, K), "pair_row")
+    dev = _device_of(dout, "dout")
+    _expect(dout, torch.bfloat16, (T, d), dev, "dout")
+    _expect(x, torch.bfloat16, (T, d), dev, "x")
+    _expect(y, torch.bfloat16, (rows, d), dev, "y")
+    _expect(gate, torch.float32, (T, K), dev, "gate")
+    _expect(pair_row, torch.int32, (T, K), dev, "pair_row")
+    if dy is not None:
+        _expect(dy, torch.bfloat16, (rows, d), dev, "dy")
+    if dgate is not None:
+        _expect(dgate, torch.float32, (T, K), dev, "dgate")
+    if dx is not None:
+        _expect(dx, torch.bfloat16, (T, d), dev, "dx")
     with _alloc_on(stream):
         if dy is None:
-            dy = torch.zeros_like(y)
+            dy = torch.zeros(rows, d, dtype=torch.bfloat16, device=dev)
         if dgate is None:
-            dgate = torch.empty(T, K, dtype=torch.float32, device=dout.device)
+            dgate = torch.empty(T, K, dtype=torch.float32, device=dev)
         if dx is None:
-            dx = torch.empty_like(dout)
+            dx = torch.empty(T, d, dtype=torch.bfloat16, device=dev)
         if ws is None:
-            ws = _status_ws(dout.device)
-    _need(dy, torch.bfloat16, (rows, d), "dy")
-    _need(dgate, torch.float32, (T, K), "dgate")
-    _need(dx, torch.bfloat16, (T, d), "dx")
+            ws = _status_ws(dev)
+    _expect_ws(ws, dev)
     s = Shape(T, d, 1, K, K, 64)
-    _check(_lib().lc_moe_combine_backward(ctypes.byref(s), _ptr(dout), _ptr(x), _ptr(y), rows, _ptr(gate),
-                                          _ptr(pair_row), _ptr(dy), _ptr(dgate), _ptr(dx), _ptr(ws), ws.numel(),
-                                          _stream(stream)), "lc_moe_combine_backward")
+    _check(_lib().lc_moe_combine_backward(ctypes.byref(s), dout.data_ptr(), x.data_ptr(), y.data_ptr(), rows,
+                                          gate.data_ptr(), pair_row.data_ptr(), dy.data_ptr(), dgate.data_ptr(),
+                                          dx.data_ptr(), ws.data_ptr(), ws.nbytes, _raw_stream(stream, dev)),
+           "lc_moe_combine_backward")
     return dy, dgate, dx
 
 
@@ -649,26 +701,29 @@ def lc_moe_quantize_w4(src, group: int = 64, codes=None, scale=None, stream=None
     (codes uint8 [..., rows, cols / 2], scale bf16 [..., rows / 16, cols / group, 16])."""
     if src.dim() < 2:
         raise ValueError("src: expected [..., rows, cols]")
-    _one_device(src=src, codes=codes, scale=scale)
+    dev = _device_of(src, "src")
     *lead, rows, cols = src.shape
-    _need(src, torch.bfloat16, tuple(src.shape), "src")
+    _expect(src, torch.bfloat16, tuple(src.shape), dev, "src")
     if group not in (32, 64, 128) or rows % 16 or cols % 64 or cols % group:
         raise ValueError(f"src: rows % 16, cols % 64 and cols % group (32, 64 or 128) must be 0, got {rows} x {cols}, "
                          f"group {group}")
+    if codes is not None:
+        _expect(codes, torch.uint8, (*lead, rows, cols // 2), dev, "codes")
+    if scale is not None:
+        _expect(scale, torch.bfloat16, (*lead, rows // 16, cols // group, 16), dev, "scale")
     with _alloc_on(stream):
         if codes is None:
-            codes = torch.empty(*lead, rows, cols // 2, dtype=torch.uint8, device=src.device)
+            codes = torch.empty(*lead, rows, cols // 2, dtype=torch.uint8, device=dev)
         if scale is None:
-            scale = torch.empty(*lead, rows // 16, cols // group, 16, dtype=torch.bfloat16, device=src.device)
-    _need(codes, torch.uint8, (*lead, rows, cols // 2), "codes")
-    _need(scale, torch.bfloat16, (*lead, rows // 16, cols // group, 16), "scale")
+            scale = torch.empty(*lead, rows // 16, cols // group, 16, dtype=torch.bfloat16, device=dev)
     if src.numel():
-        _check(_lib().lc_moe_quantize_w4(_ptr(src), src.numel() // cols, cols, group, _ptr(codes), _ptr(scale),
-                                         _stream(stream)), "lc_moe_quantize_w4")
+        _check(_lib().lc_moe_quantize_w4(src.data_ptr(), src.numel() // cols, cols, group, codes.data_ptr(),
+                                         scale.data_ptr(), _raw_stream(stream, dev)), "lc_moe_quantize_w4")
     return codes, scale
 
 
-def _w4_dims(w13q, w13_scale, w2q, w2_scale):
+def _w4_dims(w13q, w13_scale, w2q, w2_scale, dev):
+    """(N, d, I, group) of 4-bit experts on ``dev``."""
     N, two_i, half_d = _dims_of(w13q, 3, "w13q")
     I, d = two_i // 2, 2 * half_d
     groups = _dims_of(w13_scale, 4, "w13_scale")[2]
@@ -677,10 +732,10 @@ def _w4_dims(w13q, w13_scale, w2q, w2_scale):
     group = d // groups
     if group not in (32, 64, 128) or d % group or I % group:
         raise ValueError(f"w13_scale: groups of {group} columns, expected 32, 64 or 128 that divide d = {d} and I = {I}")
-    _need(w13q, torch.uint8, (N, 2 * I, d // 2), "w13q")
-    _need(w13_scale, torch.bfloat16, (N, 2 * I // 16, d // group, 16), "w13_scale")
-    _need(w2q, torch.uint8, (N, d, I // 2), "w2q")
-    _need(w2_scale, torch.bfloat16, (N, d // 16, I // group, 16), "w2_scale")
+    _expect(w13q, torch.uint8, (N, 2 * I, d // 2), dev, "w13q")
+    _expect(w13_scale, torch.bfloat16, (N, 2 * I // 16, d // group, 16), dev, "w13_scale")
+    _expect(w2q, torch.uint8, (N, d, I // 2), dev, "w2q")
+    _expect(w2_scale, torch.bfloat16, (N, d // 16, I // group, 16), dev, "w2_scale")
     return N, d, I, group
 
 
@@ -688,25 +743,28 @@ def lc_moe_expert_ffn_w4(x_perm, offsets, w13q, w13_scale, w2q, w2_scale, T: int
                          stream=None):
     """lc_moe_expert_ffn with 4-bit experts (codes and scales as lc_moe_quantize_w4 makes them).
     Returns (h, y); rows behind offsets[N] are not written."""
-    _one_device(x_perm=x_perm, offsets=offsets, w13q=w13q, w13_scale=w13_scale, w2q=w2q, w2_scale=w2_scale, h=h, y=y,
-                ws=ws)
-    N, d, I, group = _w4_dims(w13q, w13_scale, w2q, w2_scale)
+    dev = _device_of(x_perm, "x_perm")
+    N, d, I, group = _w4_dims(w13q, w13_scale, w2q, w2_scale, dev)
     rows = T * K
-    _need(x_perm, torch.bfloat16, (rows, d), "x_perm")
-    _need(offsets, torch.int32, (N + 1,), "offsets")
+    _expect(x_perm, torch.bfloat16, (rows, d), dev, "x_perm")
+    _expect(offsets, torch.int32, (N + 1,), dev, "offsets")
+    if h is not None:
+        _expect(h, torch.bfloat16, (rows, I), dev, "h")
+    if y is not None:
+        _expect(y, torch.bfloat16, (rows, d), dev, "y")
     with _alloc_on(stream):
         if h is None:
-            h = torch.empty(rows, I, dtype=torch.bfloat16, device=x_perm.device)
+            h = torch.empty(rows, I, dtype=torch.bfloat16, device=dev)
         if y is None:
-            y = torch.empty(rows, d, dtype=torch.bfloat16, device=x_perm.device)
+            y = torch.empty(rows, d, dtype=torch.bfloat16, device=dev)
         if ws is None:
-            ws = _status_ws(x_perm.device)
-    _need(h, torch.bfloat16, (rows, I), "h")
-    _need(y, torch.bfloat16, (rows, d), "y")
+            ws = _status_ws(dev)
+    _expect_ws(ws, dev)
     s = Shape(T, d, N, max(0, K - N), K, I)
-    _check(_lib().lc_moe_expert_ffn_w4(ctypes.byref(s), _ptr(x_perm), _ptr(offsets), _ptr(w13q), _ptr(w13_scale),
-                                       _ptr(w2q), _ptr(w2_scale), group, _ptr(h), _ptr(y), _ptr(ws), ws.numel(),
-                                       _stream(stream)), "lc_moe_expert_ffn_w4")
+    _check(_lib().lc_moe_expert_ffn_w4(ctypes.byref(s), x_perm.data_ptr(), offsets.data_ptr(), w13q.data_ptr(),
+                                       w13_scale.data_ptr(), w2q.data_ptr(), w2_scale.data_ptr(), group, h.data_ptr(),
+                                       y.data_ptr(), ws.data_ptr(), ws.nbytes, _raw_stream(stream, dev)),
+           "lc_moe_expert_ffn_w4")
     return h, y
 
 
@@ -717,33 +775,34 @@ def lc_moe_forward_w4(x, wr, bias, w13q, w13_scale, w2q, w2_scale, K: int, opts:
     Returns ``out`` [T, d] bf16."""
     T, d = _dims_of(x, 2, "x")
     E = _dims_of(wr, 2, "wr")[0]
-    _one_device(x=x, wr=wr, bias=bias, w13q=w13q, w13_scale=w13_scale, w2q=w2q, w2_scale=w2_scale, out=out, idx=idx,
-                gate=gate, counts=counts, ws=ws)
-    N, dw, I, group = _w4_dims(w13q, w13_scale, w2q, w2_scale)
+    dev = _device_of(x, "x")
+    N, dw, I, group = _w4_dims(w13q, w13_scale, w2q, w2_scale, dev)
     o = None
     if opts is not None:
         o = _gate_opts(**{**dict(score="softmax", groups=1, top_groups=1, group_rank=1, renorm=True, scale=1.0), **opts})
-    _need(x, torch.bfloat16, (T, dw), "x")
-    _need(wr, torch.bfloat16, (E, dw), "wr")
+    _expect(x, torch.bfloat16, (T, dw), dev, "x")
+    _expect(wr, torch.bfloat16, (E, dw), dev, "wr")
     if bias is not None:
-        _need(bias, torch.float32, (E,), "bias")
+        _expect(bias, torch.float32, (E,), dev, "bias")
     elif opts is None:
         raise ValueError("bias: required without opts")
+    if out is not None:
+        _expect(out, torch.bfloat16, (T, d), dev, "out")
+    if idx is not None:
+        _expect(idx, torch.int32, (T, K), dev, "idx")
+    if gate is not None:
+        _expect(gate, torch.float32, (T, K), dev, "gate")
+    if counts is not None:
+        _expect(counts, torch.int32, (E,), dev, "counts")
     s = Shape(T, d, N, E - N, K, I)
     with _alloc_on(stream):
         if out is None:
-            out = torch.empty(T, d, dtype=torch.bfloat16, device=x.device)
+            out = torch.empty(T, d, dtype=torch.bfloat16, device=dev)
         if ws is None:
-            ws = new_workspace(s, OP_FORWARD_W4, x.device)
-    _need(out, torch.bfloat16, (T, d), "out")
-    if idx is not None:
-        _need(idx, torch.int32, (T, K), "idx")
-    if gate is not None:
-        _need(gate, torch.float32, (T, K), "gate")
-    if counts is not None:
-        _need(counts, torch.int32, (E,), "counts")
-    _check(_lib().lc_moe_forward_w4(ctypes.byref(s), None if o is None else ctypes.byref(o), _ptr(x), _ptr(wr),
-                                    _ptr(bias), _ptr(w13q), _ptr(w13_scale), _ptr(w2q), _ptr(w2_scale), group,
-                                    _ptr(out), _ptr(idx), _ptr(gate), _ptr(counts), _ptr(ws), ws.numel(),
-                                    _stream(stream)), "lc_moe_forward_w4")
+            ws = new_workspace(s, OP_FORWARD_W4, dev)
+    _expect_ws(ws, dev)
+    _check(_lib().lc_moe_forward_w4(ctypes.byref(s), None if o is None else ctypes.byref(o), x.data_ptr(), wr.data_ptr(),
+                                    _addr(bias), w13q.data_ptr(), w13_scale.data_ptr(), w2q.data_ptr(),
+                                    w2_scale.data_ptr(), group, out.data_ptr(), _addr(idx), _addr(gate), _addr(counts),
+                                    ws.data_ptr(), ws.nbytes, _raw_stream(stream, dev)), "lc_moe_forward_w4")
     return out

@@ -99,13 +99,15 @@ __device__ __forceinline__ float redux_min(float v) {
 
 // The 32 lanes' values in descending order over the lanes (bitonic network).
 __device__ __forceinline__ float sort_descending(float v) {
-    const int lane = threadIdx.x & 31;
+    const uint32_t lane = threadIdx.x & 31;
 #pragma unroll
-    for (int k = 2; k <= 32; k *= 2)
+    for (uint32_t k = 2; k <= 32; k *= 2)
 #pragma unroll
-        for (int j = k / 2; j; j /= 2) {
+        for (uint32_t j = k / 2; j; j /= 2) {
             const float w = __shfl_xor_sync(FULL, v, j);
-            v = ((lane & j) == 0) == ((lane & k) == 0) ? fmaxf(v, w) : fminf(v, w);
+            // the larger value to the lane where bits j and k of the lane's number agree
+            const bool larger = ((lane / j ^ lane / k) & 1u) == 0;
+            v = larger ? fmaxf(v, w) : fminf(v, w);
         }
     return v;
 }
@@ -127,16 +129,11 @@ __device__ __forceinline__ double score64(float z, float m, double S, bool sigmo
     return z == m && m < 0.0f && isinf(m) ? 0.0 : exp(static_cast<double>(z) - m) / S;
 }
 
-// The whole choice in 64 bits, for any row (K rounds of a warp-wide maximum over the keys, which
-// lie in the warp's shared-memory row): lane r < K returns its pick, or -1 in every lane where a key
-// or a group's score is NaN.
+// A row's keys in 64 bits into the warp's shared-memory row; returns whether one is NaN (in any lane).
 template <class LT>
-__device__ __noinline__ int pick64(const LT* zt, const float* bias, int E, int K, const lc_moe_gate_opts& o,
-                                   float m, double* key) {
+__device__ __noinline__ bool keys64(const LT* zt, const float* bias, int E, bool sigmoid, float m, double* key) {
     const int lane = threadIdx.x & 31;
-    const bool sigmoid = o.score == LC_MOE_SCORE_SIGMOID;
     const double S = sigmoid ? 1.0 : softmax_sum64(zt, E, m);
-    const int size = E / o.groups;
     bool nan = false;
     __syncwarp();
     for (int i = lane; i < E; i += 32) {
@@ -146,43 +143,49 @@ __device__ __noinline__ int pick64(const LT* zt, const float* bias, int E, int K
         key[i] = k;
     }
     __syncwarp();
-    uint32_t kept = FULL;  // bit g: group g stays
-    if (o.top_groups < o.groups) {
-        unsigned long long mine = 0;  // lane g: the ordered score of group g
-        for (int g = 0; g < o.groups; ++g) {
-            double a = -INFINITY, b = -INFINITY;
-            for (int i = lane; i < size; i += 32) {
-                const double k = key[g * size + i];
-                if (k > a) { b = a; a = k; }
-                else if (k > b) b = k;
-            }
-#pragma unroll
-            for (int w = 16; w; w >>= 1) {
-                const double a2 = __shfl_xor_sync(FULL, a, w), b2 = __shfl_xor_sync(FULL, b, w);
-                b = fmax(fmin(a, a2), fmax(b, b2));
-                a = fmax(a, a2);
-            }
-            const double score = o.group_rank == 2 && size > 1 ? a + b : a;
-            nan |= score != score;
-            if (lane == g) mine = ordered(score);
+    return __any_sync(FULL, nan);
+}
+
+// The groups that stay, decided in 64 bits from the keys in shared memory: bit g for group g (0
+// where a group's score is NaN).
+__device__ __noinline__ uint32_t groups64(const double* key, const lc_moe_gate_opts& o, int size, int team) {
+    const int lane = threadIdx.x & 31, g = lane / team;
+    double a = -INFINITY, b = -INFINITY;
+    if (g < o.groups)
+        for (int i = lane % team; i < size; i += team) {
+            const double k = key[g * size + i];
+            b = fmax(b, fmin(a, k));
+            a = fmax(a, k);
         }
-        kept = 0;
-        for (int r = 0; r < o.top_groups; ++r) {
-            const int g = arg_max(mine, lane);
-            kept |= 1u << g;
-            if (lane == g) mine = 0;
-        }
+    for (int w = 1; w < team; w <<= 1) {
+        const double a2 = __shfl_xor_sync(FULL, a, w), b2 = __shfl_xor_sync(FULL, b, w);
+        b = fmax(fmin(a, a2), fmax(b, b2));
+        a = fmax(a, a2);
     }
-    if (__any_sync(FULL, nan)) return -1;
-    unsigned long long taken = 0, best = 0;
+    double score = o.group_rank == 2 && size > 1 ? a + b : a;
+    score = __shfl_sync(FULL, score, (lane * team) & 31);  // lane g: group g
+    if (__any_sync(FULL, lane < o.groups && score != score)) return 0;
+    int rank = 0;
+    for (int q = 0; q < o.groups; ++q) {
+        const double other = __shfl_sync(FULL, score, q);
+        rank += other > score || (other == score && q < lane);
+    }
+    return __ballot_sync(FULL, lane < o.groups && rank < o.top_groups);
+}
+
+// K picks from the 64-bit keys in shared memory, for any row: K rounds of a warp-wide maximum over
+// each lane's largest key that is left. Lane r < K returns its pick. The keys are overwritten.
+__device__ __noinline__ int pick64(double* key, int E, int K, uint32_t kept, int size) {
+    const int lane = threadIdx.x & 31;
+    unsigned long long* left = reinterpret_cast<unsigned long long*>(key);
+    for (int i = lane; i < E; i += 32) left[i] = (kept >> (i / size)) & 1u ? ordered(key[i]) : 0ull;
+    unsigned long long best = 0;
     int at = 0x7fffffff, my_idx = 0;
-    auto offer = [&]() {  // this lane's best untaken key
+    auto offer = [&]() {
         best = 0;
         at = 0x7fffffff;
-        for (int i = lane, j = 0; i < E; i += 32, ++j) {
-            if ((taken >> j) & 1) continue;
-            if (o.top_groups < o.groups && !((kept >> (i / size)) & 1u)) continue;
-            const unsigned long long k = ordered(key[i]);
+        for (int i = lane; i < E; i += 32) {
+            const unsigned long long k = left[i];
             if (k > best) {
                 best = k;
                 at = i;
@@ -194,7 +197,7 @@ __device__ __noinline__ int pick64(const LT* zt, const float* bias, int E, int K
         const int w = arg_max(best, at);
         if (lane == r) my_idx = w;
         if ((w & 31) == lane) {
-            taken |= 1ull << (w >> 5);
+            left[w] = 0;
             offer();
         }
     }
@@ -210,17 +213,25 @@ __device__ __noinline__ int pick64(const LT* zt, const float* bias, int E, int K
 //   Scores below e^-87 count as 0 (1e-37 covers them); key = s + b adds u |key|.
 constexpr float U23 = 1.1920929e-07f;
 
-template <class LT, int VPL>
-__global__ void __launch_bounds__(GATE_THREADS)
+// team: lanes to a group when group scores are taken (a power of two, so that all groups run at once);
+// a group's keys start size + pad words apart in the warp's row of row_len doubles, so that the
+// teams' reads fall on different banks.
+// CTAs to an SM: 64 registers a thread hold up to 12 keys a lane without spills, more keys want 128
+// (16384 x 768: 33.3 us with 2 CTAs, 33.7 with 3, 34.2 with 4).
+constexpr int gate_ctas(int vpl) { return vpl <= 12 ? 4 : 2; }
+
+// FILLED: E is 32 VPL.
+template <class LT, int VPL, bool FILLED>
+__global__ void __launch_bounds__(VPL <= 32 ? 256 : 128, gate_ctas(VPL))
     gate_kernel(const LT* __restrict__ logits, const float* __restrict__ bias, int T, int E, int K,
-                lc_moe_gate_opts o, int32_t* __restrict__ idx, float* __restrict__ gate,
-                int32_t* __restrict__ counts, uint32_t* __restrict__ status) {
+                lc_moe_gate_opts o, int team, int pad, int row_len, int32_t* __restrict__ idx,
+                float* __restrict__ gate, int32_t* __restrict__ counts, uint32_t* __restrict__ status) {
     extern __shared__ double s_dyn[];
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, warps = blockDim.x >> 5;
-    double* row64 = s_dyn + static_cast<size_t>(warp) * max(E, 32);  // this warp's keys, or its candidates
+    double* row64 = s_dyn + static_cast<size_t>(warp) * row_len;  // this warp's keys, or its candidates
     float* row32 = reinterpret_cast<float*>(row64);
     int32_t* cand = reinterpret_cast<int32_t*>(row64);
-    int32_t* s_hist = reinterpret_cast<int32_t*>(s_dyn + static_cast<size_t>(warps) * max(E, 32));
+    int32_t* s_hist = reinterpret_cast<int32_t*>(s_dyn + static_cast<size_t>(warps) * row_len);
     if (counts) {
         for (int i = threadIdx.x; i < E; i += blockDim.x) s_hist[i] = 0;
         __syncthreads();
@@ -231,37 +242,27 @@ __global__ void __launch_bounds__(GATE_THREADS)
     // without a bias and without sums of scores the logits themselves are in the keys' order
     const bool by_z = !bias && (!grouped || o.group_rank == 1);
     const int size = E / o.groups;
+    // i / size for i < E <= 32 size (E <= 2048): the error of the quotient stays below 1 / size
+    const uint32_t inv_size = ((1u << 22) + size - 1) / size;
+    auto group_of = [&](int i) { return static_cast<int>((static_cast<uint32_t>(i) * inv_size) >> 22); };
+    bool bias_nan = false;
     float bmin = 0.0f;  // the smallest finite bias: score = key - b <= key - bmin
     if (bias) {
         bmin = __int_as_float(0x7f800000);
         for (int i = lane; i < E; i += 32) {
             const float b = __ldg(bias + i);
             if (b > NEG_INF) bmin = fminf(bmin, b);
+            bias_nan |= b != b;
         }
         bmin = redux_min(bmin);
     }
-    constexpr bool PREFETCH = VPL <= 32;
-    float vn[PREFETCH ? VPL : 1];
-    auto load = [&](int tt, float* dst) {
-        const LT* z = logits + static_cast<int64_t>(tt) * E;
-#pragma unroll
-        for (int j = 0; j < VPL; ++j) {
-            const int i = lane + 32 * j;
-            dst[j] = (tt < T && i < E) ? load_logit(z + i) : NEG_INF;
-        }
-    };
     const int stride = gridDim.x * warps;
-    if (PREFETCH) load(blockIdx.x * warps + warp, vn);
+    auto in = [&](int j) { return FILLED || lane + 32 * j < E; };  // whether place j of this lane is an expert
     for (int t = blockIdx.x * warps + warp; t < T; t += stride) {
         const LT* zt = logits + static_cast<int64_t>(t) * E;
         float v[VPL];
-        if (PREFETCH) {
 #pragma unroll
-            for (int j = 0; j < VPL; ++j) v[j] = vn[PREFETCH ? j : 0];
-            load(t + stride, vn);
-        } else {
-            load(t, v);
-        }
+        for (int j = 0; j < VPL; ++j) v[j] = in(j) ? load_logit(zt + lane + 32 * j) : NEG_INF;
         float m = NEG_INF, S = 1.0f, inv_S = 1.0f;
         bool nan = false;
         if (!sigmoid) {
@@ -279,28 +280,34 @@ __global__ void __launch_bounds__(GATE_THREADS)
 #pragma unroll
                 for (int j = 0; j < VPL; ++j) part += __expf(v[j] - m0);
                 S = warp_sum(part);
-                inv_S = S > 0.0f ? 1.0f / S : 0.0f;
+                inv_S = S > 0.0f ? __fdividef(1.0f, S) : 0.0f;
             }
         } else {
+            float part = 0.0f;  // NaN where a logit is
             if (sigmoid) {
 #pragma unroll
-                for (int j = 0; j < VPL; ++j) v[j] = __fdividef(1.0f, 1.0f + __expf(-v[j]));
+                for (int j = 0; j < VPL; ++j) {
+                    v[j] = __fdividef(1.0f, 1.0f + __expf(-v[j]));
+                    part += v[j];
+                }
             } else {
-                float part = 0.0f;
 #pragma unroll
                 for (int j = 0; j < VPL; ++j) {
                     v[j] = __expf(v[j] - m0);
                     part += v[j];
                 }
                 S = warp_sum(part);
-                inv_S = S > 0.0f || S != S ? 1.0f / S : 0.0f;
+                inv_S = S > 0.0f || S != S ? __fdividef(1.0f, S) : 0.0f;
             }
+            nan = bias_nan || part != part;
+            // a place past E has score 0 and key -inf
+            if (bias) {
 #pragma unroll
-            for (int j = 0; j < VPL; ++j) {
-                const int i = lane + 32 * j;
-                const float b = bias && i < E ? __ldg(bias + i) : 0.0f;
-                v[j] = i < E ? fmaf(v[j], inv_S, b) : NEG_INF;
-                nan |= v[j] != v[j];
+                for (int j = 0; j < VPL; ++j)
+                    v[j] = fmaf(v[j], inv_S, in(j) ? __ldg(bias + lane + 32 * j) : NEG_INF);
+            } else {
+#pragma unroll
+                for (int j = 0; j < VPL; ++j) v[j] = fmaf(v[j], inv_S, in(j) ? 0.0f : NEG_INF);
             }
         }
         // bound on the error of a key k whose score is at most top
@@ -313,21 +320,20 @@ __global__ void __launch_bounds__(GATE_THREADS)
             const float rel = (sigmoid ? 0x1p-16f : 0x1p-15f) * (k - bmin), all = (sigmoid ? 7.0f : 36.0f * inv_S) * U23;
             return fminf(rel, all) + U23 * fabsf(k) + 1e-37f;
         };
-        bool sure = !__any_sync(FULL, nan);
-        if (grouped && sure) {
+        // kept: the groups that stay (0: a key or a group's score is NaN)
+        uint32_t kept = __any_sync(FULL, nan) ? 0u : FULL;
+        if (grouped && kept) {
             // group scores: teams of lanes over the keys in shared memory
             __syncwarp();
 #pragma unroll
             for (int j = 0; j < VPL; ++j)
-                if (lane + 32 * j < E) row32[lane + 32 * j] = v[j];
+                if (in(j)) row32[lane + 32 * j + group_of(lane + 32 * j) * pad] = v[j];
             __syncwarp();
-            int team = 32;  // lanes to a group: a power of two, so that all groups run at once
-            while (team * o.groups > 32) team >>= 1;
             const int g = lane / team, part = lane % team;
             float a = NEG_INF, b = NEG_INF;
             if (g < o.groups)
                 for (int i = part; i < size; i += team) {
-                    const float k = row32[g * size + i];
+                    const float k = row32[g * (size + pad) + i];
                     b = fmaxf(b, fminf(a, k));
                     a = fmaxf(a, k);
                 }
@@ -348,20 +354,23 @@ __global__ void __launch_bounds__(GATE_THREADS)
                 const float other = __shfl_sync(FULL, score, q);
                 rank += other > score || (other == score && q < lane);
             }
-            const uint32_t kept = __ballot_sync(FULL, lane < o.groups && rank < o.top_groups);
+            kept = __ballot_sync(FULL, lane < o.groups && rank < o.top_groups);
             // the groups that stay and those that leave are apart by their bounds (infinite scores have no
             // bound and are what they are in 64 bits)
             const float low = redux_min(((kept >> lane) & 1u) ? score - err : __int_as_float(0x7f800000));
             const float high = redux_max(lane < o.groups && !((kept >> lane) & 1u) ? score + err : NEG_INF);
-            sure = low > high && !__any_sync(FULL, score != score);
+            if (!(low > high) || __any_sync(FULL, score != score)) {
+                keys64(zt, bias, E, sigmoid, m, row64);
+                kept = groups64(row64, o, size, team);
+            }
 #pragma unroll
             for (int j = 0; j < VPL; ++j) {
                 const int i = lane + 32 * j;
-                if (i < E && !((kept >> (i / size)) & 1u)) v[j] = NEG_INF;
+                if (in(j) && !((kept >> group_of(i)) & 1u)) v[j] = NEG_INF;
             }
         }
         int total = 0;
-        if (sure) {
+        if (kept) {
             // the K-th largest of the lanes' largest keys is at most the K-th largest key
             float top = NEG_INF;
 #pragma unroll
@@ -369,9 +378,13 @@ __global__ void __launch_bounds__(GATE_THREADS)
             const float tau = __shfl_sync(FULL, sort_descending(top), K - 1);
             const float least = tau - 2.0f * error_of(tau) - U23 * fabsf(tau);
             if (least > NEG_INF) {
+                // bits of the places that hold candidates: low and high half of VPL
+                uint32_t bits[(VPL + 31) / 32] = {};
+#pragma unroll
+                for (int j = 0; j < VPL; ++j) bits[j / 32] |= v[j] >= least ? 1u << (j % 32) : 0u;
                 int mine = 0;
 #pragma unroll
-                for (int j = 0; j < VPL; ++j) mine += v[j] >= least;
+                for (int h = 0; h < (VPL + 31) / 32; ++h) mine += __popc(bits[h]);
                 int before = mine;
 #pragma unroll
                 for (int w = 1; w < 32; w <<= 1) {
@@ -380,11 +393,14 @@ __global__ void __launch_bounds__(GATE_THREADS)
                 }
                 total = __shfl_sync(FULL, before, 31);
                 __syncwarp();
-                if (total <= 32 && mine) {
+                if (total <= 32) {
                     before -= mine;
 #pragma unroll
-                    for (int j = 0; j < VPL; ++j)
-                        if (v[j] >= least) cand[before++] = lane + 32 * j;
+                    for (int h = 0; h < (VPL + 31) / 32; ++h)
+                        while (bits[h]) {
+                            cand[before++] = lane + 32 * (32 * h + __ffs(bits[h]) - 1);
+                            bits[h] &= bits[h] - 1;
+                        }
                 }
             }
         }
@@ -412,6 +428,7 @@ __global__ void __launch_bounds__(GATE_THREADS)
                 }
             }
             int rank = 0;
+#pragma unroll 4
             for (int q = 0; q < total; ++q) {
                 const float kq = __shfl_sync(FULL, k, q);
                 const int iq = __shfl_sync(FULL, i, q);
@@ -429,8 +446,10 @@ __global__ void __launch_bounds__(GATE_THREADS)
             const float z_n = __shfl_down_sync(FULL, z_s, 1), b_n = __shfl_down_sync(FULL, b_s, 1);
             const bool close = lane < K && lane + 1 < total && !(k_s - k_n > e_s + e_n) && !(z_s == z_n && b_s == b_n);
             my_idx = i_s;
+            z = z_s;
             if (__any_sync(FULL, close)) {
                 const double S64 = sigmoid ? 1.0 : softmax_sum64(zt, E, m);
+                z = lane < total ? load_logit(zt + i) : NEG_INF;
                 const double k64 = lane < total ? score64(z, m, S64, sigmoid) + static_cast<double>(b) : -INFINITY;
                 rank = 0;
                 for (int q = 0; q < total; ++q) {
@@ -442,18 +461,21 @@ __global__ void __launch_bounds__(GATE_THREADS)
                 if (lane < total) cand[rank] = i;
                 __syncwarp();
                 my_idx = lane < total ? cand[lane] : 0;
+                z = load_logit(zt + my_idx);
             }
         } else {
-            my_idx = pick64(zt, bias, E, K, o, m, row64);
+            const bool nan64 = keys64(zt, bias, E, sigmoid, m, row64);
+            if (nan64) kept = 0;
+            else if (grouped && !kept) kept = groups64(row64, o, size, team);
+            else if (!kept) kept = FULL;
+            my_idx = kept ? pick64(row64, E, K, kept, grouped ? size : E) : lane;
+            if (lane < K) z = load_logit(zt + my_idx);
         }
         __syncwarp();
-        const bool bad = my_idx < 0;  // in every lane
-        if (bad) {
-            my_idx = lane;
-            if (lane == 0) set_status(status, LC_MOE_DEV_NAN_KEY);
-        }
+        const bool bad = !kept;
+        if (bad && lane == 0) set_status(status, LC_MOE_DEV_NAN_KEY);
         // gates, from the chosen logits
-        z = lane < K ? load_logit(zt + my_idx) : NEG_INF;
+        if (lane >= K) z = NEG_INF;
         float g;
         if (o.renorm) g = chosen_share(z, sigmoid);
         else if (sigmoid) g = sigmoid32(z);
@@ -517,7 +539,7 @@ __global__ void __launch_bounds__(GATE_THREADS)
             float part = 0.0f;
             for (int j = lane; j < E; j += 32) part += expf(load_logit(zt + j) - m);
             const float S = warp_sum(part);
-            inv_S = S > 0.0f || S != S ? 1.0f / S : 0.0f;
+            inv_S = S > 0.0f || S != S ? __fdividef(1.0f, S) : 0.0f;
             const float s = i >= 0 ? expf(z - m) * inv_S : 0.0f;
             D = warp_sum(s * dg);
             mine = s * dg;
@@ -545,25 +567,38 @@ __global__ void __launch_bounds__(GATE_THREADS)
 
 namespace {
 
-template <class LT, int VPL>
-cudaError_t launch_gate_t(const LT* logits, const float* bias, int T, int E, int K, const lc_moe_gate_opts& o,
+template <class LT, int VPL, bool FILLED>
+cudaError_t launch_gate_f(const LT* logits, const float* bias, int T, int E, int K, const lc_moe_gate_opts& o,
                           int32_t* idx, float* gate, int32_t* counts, uint32_t* status, cudaStream_t st) {
     const DevInfo* di = current_device_info();
     if (!di) return cudaErrorUnknown;
     constexpr int MAX_WARPS = VPL <= 32 ? 8 : 4;
-    constexpr int MAX_SMEM = MAX_WARPS * 32 * VPL * 8 + 32 * VPL * 4;
+    constexpr int MAX_SMEM = MAX_WARPS * (32 * VPL * 8 + 32 * 31 * 4) + 32 * VPL * 4;
     static PerDeviceOnce setup;
     const cudaError_t e = setup.run([](int) {
-        return cudaFuncSetAttribute(gate_kernel<LT, VPL>, cudaFuncAttributeMaxDynamicSharedMemorySize, MAX_SMEM);
+        return cudaFuncSetAttribute(gate_kernel<LT, VPL, FILLED>, cudaFuncAttributeMaxDynamicSharedMemorySize, MAX_SMEM);
     });
     if (e != cudaSuccess) return e;
     // few tokens: spread them over the SMs
     const int warps = T <= di->sm_count ? 1 : T <= 4 * di->sm_count ? 2 : MAX_WARPS;
-    const size_t smem = static_cast<size_t>(warps) * (E > 32 ? E : 32) * 8 + (counts ? static_cast<size_t>(E) * 4 : 0);
+    int team = 32;
+    while (team * o.groups > 32) team >>= 1;
+    const int pad = (team - E / o.groups) & 31;
+    int row_len = E > 32 ? E : 32;
+    if (o.top_groups < o.groups && (E + o.groups * pad + 1) / 2 > row_len) row_len = (E + o.groups * pad + 1) / 2;
+    const size_t smem = static_cast<size_t>(warps) * row_len * 8 + (counts ? static_cast<size_t>(E) * 4 : 0);
     int blocks = (T + warps - 1) / warps;
-    if (blocks > di->sm_count * 4) blocks = di->sm_count * 4;
-    gate_kernel<LT, VPL><<<blocks, warps * 32, smem, st>>>(logits, bias, T, E, K, o, idx, gate, counts, status);
+    if (blocks > di->sm_count * gate_ctas(VPL)) blocks = di->sm_count * gate_ctas(VPL);  // one wave
+    gate_kernel<LT, VPL, FILLED><<<blocks, warps * 32, smem, st>>>(logits, bias, T, E, K, o, team, pad, row_len, idx, gate,
+                                                                 counts, status);
     return cudaGetLastError();
+}
+
+template <class LT, int VPL>
+cudaError_t launch_gate_t(const LT* logits, const float* bias, int T, int E, int K, const lc_moe_gate_opts& o,
+                          int32_t* idx, float* gate, int32_t* counts, uint32_t* status, cudaStream_t st) {
+    if (E == 32 * VPL) return launch_gate_f<LT, VPL, true>(logits, bias, T, E, K, o, idx, gate, counts, status, st);
+    return launch_gate_f<LT, VPL, false>(logits, bias, T, E, K, o, idx, gate, counts, status, st);
 }
 
 template <class LT>
