@@ -101,59 +101,124 @@ __global__ void __launch_bounds__(COMBINE_THREADS)
     }
 }
 
-// One warp per (token, pick).
+__device__ __forceinline__ float dot8(const uint4& a, const uint4& b, float s) {
+    const uint32_t p[4] = {a.x, a.y, a.z, a.w}, q[4] = {b.x, b.y, b.z, b.w};
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+        s = __fmaf_rn(bf16lo(p[j]), bf16lo(q[j]), s);
+        s = __fmaf_rn(bf16hi(p[j]), bf16hi(q[j]), s);
+    }
+    return s;
+}
+
+__device__ __forceinline__ uint4 times8(float g, const uint4& v) {
+    float acc[8];
+    const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+        acc[2 * j] = g * bf16lo(w[j]);
+        acc[2 * j + 1] = g * bf16hi(w[j]);
+    }
+    return pack8(acc);
+}
+
+__device__ __forceinline__ float warp_total(float v) {
+#pragma unroll
+    for (int o = 16; o; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+    return v;
+}
+
+// A team of wpt warps per token holds the token's row of dout in registers (NC 16-byte chunks a
+// lane) and passes over its picks, two at a time: every row of Y is read once and its gradient
+// written once, dout and x are read once. Lane r keeps the sum of pick r; the warps' sums join in
+// shared memory in warp order. With few tokens blockIdx.y deals the picks out to `splits` CTAs.
+template <int NC>
 __global__ void __launch_bounds__(COMBINE_THREADS)
     combine_backward_kernel(const uint4* __restrict__ dout, const uint4* __restrict__ x,
                             const uint4* __restrict__ y, int64_t y_rows, const float* __restrict__ gate,
-                            const int32_t* __restrict__ pair_row, int64_t T, int d8, int K,
+                            const int32_t* __restrict__ pair_row, int T, int d8, int K, int wpt, int splits,
                             uint4* __restrict__ dy, float* __restrict__ dgate, uint4* __restrict__ dx,
                             uint32_t* __restrict__ status) {
+    __shared__ float s_sum[COMBINE_THREADS / 32][32];
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const int64_t warps_total = static_cast<int64_t>(gridDim.x) * (COMBINE_THREADS / 32);
-    for (int64_t it = static_cast<int64_t>(blockIdx.x) * (COMBINE_THREADS / 32) + warp; it < T * (K + 1);
-         it += warps_total) {
-        const int64_t t = it / (K + 1);
-        const int r = static_cast<int>(it - t * (K + 1));
-        const uint4* g8 = dout + t * d8;
-        if (r == K) {  // dx
-            float w = lane < K && pair_row[t * K + lane] < 0 ? gate[t * K + lane] : 0.0f;
+    const int teams = (COMBINE_THREADS / 32) / wpt, tw = warp % wpt;
+    const int64_t t = static_cast<int64_t>(blockIdx.x) * teams + warp / wpt;
+    const bool live = t < T;
+    float g = 0.0f, sum = 0.0f;
+    int row = -1;
+    if (live && lane < K) {
+        g = gate[t * K + lane];
+        row = pair_row[t * K + lane];
+    }
+    const bool mine = live && lane < K && lane % splits == static_cast<int>(blockIdx.y);
+    if (live) {
+        const bool bad = row >= y_rows;
+        if (mine && bad && tw == 0) set_status(status, LC_MOE_DEV_IDX_RANGE);
+        const uint32_t zeros = __ballot_sync(0xffffffffu, mine && row < 0);
+        const uint32_t rows = __ballot_sync(0xffffffffu, mine && row >= 0 && !bad);
+        const float g_zero = warp_total(row < 0 ? g : 0.0f);
+        for (int c0 = tw * 32 * NC + lane; c0 - lane < d8; c0 += wpt * 32 * NC) {
+            uint4 o[NC];
 #pragma unroll
-            for (int o = 16; o; o >>= 1) w += __shfl_xor_sync(0xffffffffu, w, o);
-            for (int c = lane; c < d8; c += 32) {
-                float acc[8] = {};
-                fma_row(acc, w, g8[c]);
-                dx[t * d8 + c] = pack8(acc);
-            }
-            continue;
-        }
-        const int32_t row = pair_row[t * K + r];
-        const float w = gate[t * K + r];
-        if (row >= y_rows) {
-            if (lane == 0) {
-                set_status(status, LC_MOE_DEV_IDX_RANGE);
-                dgate[t * K + r] = 0.0f;
-            }
-            continue;
-        }
-        const uint4* v8 = row < 0 ? x + t * d8 : y + row * static_cast<int64_t>(d8);
-        float dot = 0.0f;
-        for (int c = lane; c < d8; c += 32) {
-            const uint4 g = g8[c], v = v8[c];
-            const uint32_t a[4] = {g.x, g.y, g.z, g.w}, b[4] = {v.x, v.y, v.z, v.w};
+            for (int i = 0; i < NC; ++i) o[i] = c0 + 32 * i < d8 ? __ldg(dout + t * d8 + c0 + 32 * i) : make_uint4(0, 0, 0, 0);
+            if (blockIdx.y == 0) {
 #pragma unroll
-            for (int j = 0; j < 4; ++j) {
-                dot = __fmaf_rn(bf16lo(a[j]), bf16lo(b[j]), dot);
-                dot = __fmaf_rn(bf16hi(a[j]), bf16hi(b[j]), dot);
+                for (int i = 0; i < NC; ++i)
+                    if (c0 + 32 * i < d8) __stcs(dx + t * d8 + c0 + 32 * i, times8(g_zero, o[i]));
             }
-            if (row >= 0) {
-                float acc[8] = {};
-                fma_row(acc, w, g);
-                dy[row * static_cast<int64_t>(d8) + c] = pack8(acc);
+            if (zeros) {
+                float s = 0.0f;
+#pragma unroll
+                for (int i = 0; i < NC; ++i)
+                    if (c0 + 32 * i < d8) s = dot8(o[i], __ldcs(x + t * d8 + c0 + 32 * i), s);
+                s = warp_total(s);
+                if ((zeros >> lane) & 1u) sum += s;
+            }
+            for (uint32_t left = rows; left;) {
+                const int ra = __ffs(left) - 1;
+                left &= left - 1;
+                const int rb = left ? __ffs(left) - 1 : -1;  // the second pick of the pair, if there is one
+                left &= left ? left - 1 : 0;
+                const int64_t ya = static_cast<int64_t>(__shfl_sync(0xffffffffu, row, ra)) * d8;
+                const int64_t yb = static_cast<int64_t>(__shfl_sync(0xffffffffu, row, rb & 31)) * d8;
+                const float ga = __shfl_sync(0xffffffffu, g, ra), gb = __shfl_sync(0xffffffffu, g, rb & 31);
+                uint4 va[NC], vb[NC];
+#pragma unroll
+                for (int i = 0; i < NC; ++i) {
+                    va[i] = vb[i] = make_uint4(0, 0, 0, 0);
+                    if (c0 + 32 * i < d8) {
+                        va[i] = __ldcs(y + ya + c0 + 32 * i);
+                        if (rb >= 0) vb[i] = __ldcs(y + yb + c0 + 32 * i);
+                    }
+                }
+                float sa = 0.0f, sb = 0.0f;
+#pragma unroll
+                for (int i = 0; i < NC; ++i) {
+                    if (c0 + 32 * i < d8) {
+                        __stcs(dy + ya + c0 + 32 * i, times8(ga, o[i]));
+                        if (rb >= 0) __stcs(dy + yb + c0 + 32 * i, times8(gb, o[i]));
+                    }
+                    sa = dot8(o[i], va[i], sa);
+                    sb = dot8(o[i], vb[i], sb);
+                }
+                sa = warp_total(sa);
+                sb = warp_total(sb);
+                if (lane == ra) sum += sa;
+                if (lane == rb) sum += sb;
             }
         }
-#pragma unroll
-        for (int o = 16; o; o >>= 1) dot += __shfl_xor_sync(0xffffffffu, dot, o);
-        if (lane == 0) dgate[t * K + r] = dot;
+        if (bad) sum = 0.0f;
+    }
+    if (wpt == 1) {
+        if (mine) dgate[t * K + lane] = sum;
+        return;
+    }
+    s_sum[warp][lane] = sum;
+    __syncthreads();
+    if (mine && tw == 0) {
+        float all = 0.0f;
+        for (int w = 0; w < wpt; ++w) all += s_sum[warp + w][lane];
+        dgate[t * K + lane] = all;
     }
 }
 
@@ -165,12 +230,27 @@ cudaError_t launch_combine_backward(const void* dout, const void* x, const void*
     const DevInfo* di = current_device_info();
     if (!di) return cudaErrorUnknown;
     if (T == 0) return cudaSuccess;
-    const int warps = COMBINE_THREADS / 32;
-    int64_t blocks = (static_cast<int64_t>(T) * (K + 1) + warps - 1) / warps;
-    if (blocks > di->sm_count * 8) blocks = di->sm_count * 8;
-    combine_backward_kernel<<<static_cast<int>(blocks), COMBINE_THREADS, 0, st>>>(
-        static_cast<const uint4*>(dout), static_cast<const uint4*>(x), static_cast<const uint4*>(y), y_rows, gate,
-        pair_row, T, d / 8, K, static_cast<uint4*>(dy), dgate, static_cast<uint4*>(dx), status);
+    const int warps = COMBINE_THREADS / 32, d8 = d / 8;
+    // as many warps to a token as leave a lane at most 4 chunks of its row (or all 8)
+    int wpt = 1;
+    while (wpt < warps && d8 > wpt * 32 * 4) wpt *= 2;
+    const int teams = warps / wpt;
+    const int blocks = (T - 1) / teams + 1;
+    // few tokens: deal a token's picks out until there are 2 CTAs an SM
+    int splits = 1;
+    while (splits < K && blocks * splits < 2 * di->sm_count) splits *= 2;
+    if (splits > K) splits = K;
+    const int nc = (d8 + wpt * 32 - 1) / (wpt * 32);
+    const dim3 grid(blocks, splits);
+    const auto launch = [&](auto kernel) {
+        kernel<<<grid, COMBINE_THREADS, 0, st>>>(static_cast<const uint4*>(dout), static_cast<const uint4*>(x),
+                                                 static_cast<const uint4*>(y), y_rows, gate, pair_row, T, d8, K, wpt, splits,
+                                                 static_cast<uint4*>(dy), dgate, static_cast<uint4*>(dx), status);
+    };
+    if (nc == 1) launch(combine_backward_kernel<1>);
+    else if (nc == 2) launch(combine_backward_kernel<2>);
+    else if (nc == 3) launch(combine_backward_kernel<3>);
+    else launch(combine_backward_kernel<4>);
     return cudaGetLastError();
 }
 
