@@ -315,17 +315,26 @@ __global__ void __launch_bounds__(W4_THREADS, 2) w4_kernel(const W4Args a) {
     produce(Int<HALVES - 1>());
     produce(Int<0>());
 
+    // the gate/up product lets the down product start; the down product waits for it before it reads
+    // H (weights and offsets are older than both kernels)
+    if (SWIGLU) asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+    else asm volatile("griddepcontrol.wait;" ::: "memory");
+
     // ---- activations of the next step, in registers: rows g and g + 8 of the item. A row past the
     // item's last repeats the last (its column of the product is not stored).
     auto row_ptr = [&](const Item& it, int n) {
         return a.x + static_cast<int64_t>(it.row0 + min(g + 8 * n, it.rows - 1)) * a.k + (kw * 64 + 8 * t);
     };
+    // H is written while the down product is already running: no read-only loads there
+    auto load16 = [](const __nv_bfloat16* p) {
+        return SWIGLU ? __ldg(reinterpret_cast<const uint4*>(p)) : *reinterpret_cast<const uint4*>(p);
+    };
     auto load_x = [&](uint4 (&v)[MAXNT][2], const __nv_bfloat16* p, int64_t to_row8, int rows) {
-        v[0][0] = __ldg(reinterpret_cast<const uint4*>(p));
-        v[0][1] = __ldg(reinterpret_cast<const uint4*>(p + 32));
+        v[0][0] = load16(p);
+        v[0][1] = load16(p + 32);
         if (MAXNT > 1 && rows > 8) {
-            v[MAXNT - 1][0] = __ldg(reinterpret_cast<const uint4*>(p + to_row8));
-            v[MAXNT - 1][1] = __ldg(reinterpret_cast<const uint4*>(p + to_row8 + 32));
+            v[MAXNT - 1][0] = load16(p + to_row8);
+            v[MAXNT - 1][1] = load16(p + to_row8 + 32);
         }
     };
     Item it{}, nx{};
@@ -449,19 +458,44 @@ cudaError_t launch_w4_t(const W4Args& a, cudaStream_t st) {
     });
     if (e != cudaSuccess) return e;
     const size_t smem = RING_BYTES + RED_BYTES + (static_cast<size_t>(a.N) + 1) * 4;
-    w4_kernel<SWIGLU, G32, HALVES, MAXNT><<<di->sm_count * 2, W4_THREADS, smem, st>>>(a);
-    return cudaGetLastError();
+    // The down product is launched while the gate/up product still runs: its CTAs fetch their first
+    // weights as SMs become free and wait for the other kernel before they read H.
+    cudaLaunchAttribute attr;
+    attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr.val.programmaticStreamSerializationAllowed = 1;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(di->sm_count * 2);
+    cfg.blockDim = dim3(W4_THREADS);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = st;
+    cfg.attrs = &attr;
+    cfg.numAttrs = SWIGLU ? 0 : 1;
+    const cudaError_t launched = cudaLaunchKernelEx(&cfg, w4_kernel<SWIGLU, G32, HALVES, MAXNT>, a);
+    if (launched != cudaSuccess) cudaGetLastError();
+    return launched;
+}
+
+// Warps on a tile's reduction. Fewer warps mean fewer sums to join, but also fewer and longer items:
+// a split that leaves a warp 8 steps of 64 columns, raised while there are fewer than 8 items an SM
+// (one token over 8 experts, down product: 22 us with 4 warps on a tile, SPLIT8 with 8).
+int split_of(const W4Args& a, int tile_rows, int tok) {
+    const int64_t tiles = a.m / tile_rows, row_tiles = (a.rows_cap < a.N ? a.rows_cap : a.N) + a.rows_cap / tok;
+    const int steps = a.k / 64;
+    int split = 1;
+    while (split < W4_WARPS && split * 2 <= steps &&
+           (steps / split >= 16 || row_tiles * ((tiles * split + W4_WARPS - 1) / W4_WARPS) < 8 * 148))
+        split *= 2;
+    return split;
 }
 
 template <bool SWIGLU>
 cudaError_t launch_w4(W4Args a, bool few_rows, cudaStream_t st) {
-    // as many warps on a tile's reduction as leave each of them 8 steps of 64 columns
     a.code_blk = static_cast<int64_t>(a.k / 64) * 512;
     a.scale_blk = static_cast<int64_t>(a.k / a.group) * 32;
     a.code_up = SWIGLU ? a.m / 32 * a.code_blk : 2 * a.code_blk;
-    a.split = W4_WARPS;
-    while (a.split > 1 && a.k / 64 / a.split < 8) a.split /= 2;
-    if (few_rows && a.m % 128 == 0)
+    const bool wide = few_rows && a.m % 128 == 0;
+    a.split = split_of(a, wide ? 128 : 64, wide ? 8 : 16);
+    if (wide)
         return a.group == 32 ? launch_w4_t<SWIGLU, true, 2, 1>(a, st) : launch_w4_t<SWIGLU, false, 2, 1>(a, st);
     return a.group == 32 ? launch_w4_t<SWIGLU, true, 1, 2>(a, st) : launch_w4_t<SWIGLU, false, 1, 2>(a, st);
 }
