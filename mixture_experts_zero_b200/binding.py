@@ -7,7 +7,6 @@ The library is loaded on first use. If it has not been built, or the device is n
 """
 from __future__ import annotations
 
-import contextlib
 import ctypes
 import pathlib
 import threading
@@ -578,9 +577,16 @@ def _addr(t):
     return None if t is None else t.data_ptr()
 
 
-def _alloc_on(stream):
-    """Buffers that a call makes itself belong to the stream it runs on."""
-    return contextlib.nullcontext() if stream is None else torch.cuda.stream(stream)
+def _on_stream(make, stream, *args, **kw):
+    """make(*args, **kw) for a buffer that belongs to the stream the call runs on."""
+    if stream is None:
+        return make(*args, **kw)
+    with torch.cuda.stream(stream):
+        return make(*args, **kw)
+
+
+def _empty(stream, device, dtype, *shape):
+    return _on_stream(torch.empty, stream, shape, dtype=dtype, device=device)
 
 
 def _dims_of(t, n, name):
@@ -616,13 +622,12 @@ def lc_moe_gate(logits, bias, K: int, N: int, score: str = "softmax", groups: in
         _expect(idx, torch.int32, (T, K), dev, "idx")
     if gate is not None:
         _expect(gate, torch.float32, (T, K), dev, "gate")
-    with _alloc_on(stream):
-        if idx is None:
-            idx = torch.empty(T, K, dtype=torch.int32, device=dev)
-        if gate is None:
-            gate = torch.empty(T, K, dtype=torch.float32, device=dev)
-        if ws is None:
-            ws = _status_ws(dev)
+    if idx is None:
+        idx = _empty(stream, dev, torch.int32, T, K)
+    if gate is None:
+        gate = _empty(stream, dev, torch.float32, T, K)
+    if ws is None:
+        ws = _on_stream(_status_ws, stream, dev)
     _expect_ws(ws, dev)
     s = Shape(T, 64, N, E - N, K, 64)
     _check(_lib().lc_moe_gate(ctypes.byref(s), ctypes.byref(o), logits.data_ptr(), kind, _addr(bias), idx.data_ptr(),
@@ -646,11 +651,10 @@ def lc_moe_gate_backward(logits, idx, dgate, score: str = "softmax", renorm: boo
     _expect(dgate, torch.float32, (T, K), dev, "dgate")
     if dlogits is not None:
         _expect(dlogits, logits.dtype, (T, E), dev, "dlogits")
-    with _alloc_on(stream):
-        if dlogits is None:
-            dlogits = torch.empty(T, E, dtype=logits.dtype, device=dev)
-        if ws is None:
-            ws = _status_ws(dev)
+    if dlogits is None:
+        dlogits = _empty(stream, dev, logits.dtype, T, E)
+    if ws is None:
+        ws = _on_stream(_status_ws, stream, dev)
     _expect_ws(ws, dev)
     s = Shape(T, 64, E, 0, K, 64)
     _check(_lib().lc_moe_gate_backward(ctypes.byref(s), ctypes.byref(o), logits.data_ptr(), kind, idx.data_ptr(),
@@ -678,15 +682,14 @@ def lc_moe_combine_backward(dout, x, y, gate, pair_row, dy=None, dgate=None, dx=
         _expect(dgate, torch.float32, (T, K), dev, "dgate")
     if dx is not None:
         _expect(dx, torch.bfloat16, (T, d), dev, "dx")
-    with _alloc_on(stream):
-        if dy is None:
-            dy = torch.zeros(rows, d, dtype=torch.bfloat16, device=dev)
-        if dgate is None:
-            dgate = torch.empty(T, K, dtype=torch.float32, device=dev)
-        if dx is None:
-            dx = torch.empty(T, d, dtype=torch.bfloat16, device=dev)
-        if ws is None:
-            ws = _status_ws(dev)
+    if dy is None:
+        dy = _on_stream(torch.zeros, stream, rows, d, dtype=torch.bfloat16, device=dev)
+    if dgate is None:
+        dgate = _empty(stream, dev, torch.float32, T, K)
+    if dx is None:
+        dx = _empty(stream, dev, torch.bfloat16, T, d)
+    if ws is None:
+        ws = _on_stream(_status_ws, stream, dev)
     _expect_ws(ws, dev)
     s = Shape(T, d, 1, K, K, 64)
     _check(_lib().lc_moe_combine_backward(ctypes.byref(s), dout.data_ptr(), x.data_ptr(), y.data_ptr(), rows,
@@ -711,11 +714,10 @@ def lc_moe_quantize_w4(src, group: int = 64, codes=None, scale=None, stream=None
         _expect(codes, torch.uint8, (*lead, rows, cols // 2), dev, "codes")
     if scale is not None:
         _expect(scale, torch.bfloat16, (*lead, rows // 16, cols // group, 16), dev, "scale")
-    with _alloc_on(stream):
-        if codes is None:
-            codes = torch.empty(*lead, rows, cols // 2, dtype=torch.uint8, device=dev)
-        if scale is None:
-            scale = torch.empty(*lead, rows // 16, cols // group, 16, dtype=torch.bfloat16, device=dev)
+    if codes is None:
+        codes = _empty(stream, dev, torch.uint8, *lead, rows, cols // 2)
+    if scale is None:
+        scale = _empty(stream, dev, torch.bfloat16, *lead, rows // 16, cols // group, 16)
     if src.numel():
         _check(_lib().lc_moe_quantize_w4(src.data_ptr(), src.numel() // cols, cols, group, codes.data_ptr(),
                                          scale.data_ptr(), _raw_stream(stream, dev)), "lc_moe_quantize_w4")
@@ -752,13 +754,12 @@ def lc_moe_expert_ffn_w4(x_perm, offsets, w13q, w13_scale, w2q, w2_scale, T: int
         _expect(h, torch.bfloat16, (rows, I), dev, "h")
     if y is not None:
         _expect(y, torch.bfloat16, (rows, d), dev, "y")
-    with _alloc_on(stream):
-        if h is None:
-            h = torch.empty(rows, I, dtype=torch.bfloat16, device=dev)
-        if y is None:
-            y = torch.empty(rows, d, dtype=torch.bfloat16, device=dev)
-        if ws is None:
-            ws = _status_ws(dev)
+    if h is None:
+        h = _empty(stream, dev, torch.bfloat16, rows, I)
+    if y is None:
+        y = _empty(stream, dev, torch.bfloat16, rows, d)
+    if ws is None:
+        ws = _on_stream(_status_ws, stream, dev)
     _expect_ws(ws, dev)
     s = Shape(T, d, N, max(0, K - N), K, I)
     _check(_lib().lc_moe_expert_ffn_w4(ctypes.byref(s), x_perm.data_ptr(), offsets.data_ptr(), w13q.data_ptr(),
@@ -795,11 +796,10 @@ def lc_moe_forward_w4(x, wr, bias, w13q, w13_scale, w2q, w2_scale, K: int, opts:
     if counts is not None:
         _expect(counts, torch.int32, (E,), dev, "counts")
     s = Shape(T, d, N, E - N, K, I)
-    with _alloc_on(stream):
-        if out is None:
-            out = torch.empty(T, d, dtype=torch.bfloat16, device=dev)
-        if ws is None:
-            ws = new_workspace(s, OP_FORWARD_W4, dev)
+    if out is None:
+        out = _empty(stream, dev, torch.bfloat16, T, d)
+    if ws is None:
+        ws = _on_stream(new_workspace, stream, s, OP_FORWARD_W4, dev)
     _expect_ws(ws, dev)
     _check(_lib().lc_moe_forward_w4(ctypes.byref(s), None if o is None else ctypes.byref(o), x.data_ptr(), wr.data_ptr(),
                                     _addr(bias), w13q.data_ptr(), w13_scale.data_ptr(), w2q.data_ptr(),

@@ -204,64 +204,116 @@ struct Int {
     static constexpr int value = V;
 };
 
+constexpr int W4_CTAS = 2;  // to an SM
+// ring, partial sums, prefix sums and numbers of the live experts
+constexpr size_t w4_smem(int n) { return RING_BYTES + RED_BYTES + (n + 1) * 4 + n * 2; }
+
 // Item: `8 / split` tiles of 64 HALVES weight rows of one expert (as many gate as up rows, or output
 // features) times up to 8 MAXNT of its rows. The CTA's warps form 8 / split teams, one for each
 // tile; a team's warps take every split-th step of 64 columns and join their sums in shared memory.
 // Each warp streams its codes and scales through a ring of its own (cp.async, no barriers), which
 // runs on across items; the activations of the next step are loaded into registers a step ahead.
 template <bool SWIGLU, bool G32, int HALVES, int MAXNT>
-__global__ void __launch_bounds__(W4_THREADS, 2) w4_kernel(const W4Args a) {
+__global__ void __launch_bounds__(W4_THREADS, W4_CTAS) w4_kernel(const W4Args a) {
     constexpr int TOK = 8 * MAXNT;
     extern __shared__ __align__(128) uint8_t s_raw[];
     float* red = reinterpret_cast<float*>(s_raw + RING_BYTES);
-    int32_t* pre = reinterpret_cast<int32_t*>(s_raw + RING_BYTES + RED_BYTES);  // [N + 1] row-tile prefix sums
+    // the experts that have rows: [live + 1] prefix sums of their row tiles, [live] their numbers
+    int32_t* pre = reinterpret_cast<int32_t*>(s_raw + RING_BYTES + RED_BYTES);
+    uint16_t* ids = reinterpret_cast<uint16_t*>(pre + a.N + 1);
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int g = lane >> 2, t = lane & 3;
-    if (warp == 0) {
-        int run = 0;
-        if (lane == 0) pre[0] = 0;
-        for (int base = 0; base < a.N; base += 32) {
-            const int e = base + lane;
-            int n = 0;
-            if (e < a.N) {
-                const int lo = a.offsets[e], hi = a.offsets[e + 1];
-                if (lo < 0 || hi < lo || hi > a.rows_cap) set_status(a.status, LC_MOE_DEV_IDX_RANGE);
-                else n = (hi - lo + TOK - 1) / TOK;
-            }
+    int live, row_tiles;
+    {
+        // each thread counts up to 8 consecutive experts, then a scan over the CTA (N <= 2048)
+        int32_t* part = reinterpret_cast<int32_t*>(red);  // [2][W4_WARPS]
+        const int per = (a.N + W4_THREADS - 1) / W4_THREADS, first = threadIdx.x * per;
+        int rt[8], sum = 0, some = 0;
 #pragma unroll
-            for (int o = 1; o < 32; o <<= 1) {
-                const int v = __shfl_up_sync(FULL, n, o);
-                if (lane >= o) n += v;
+        for (int i = 0; i < 8; ++i) {
+            rt[i] = 0;
+            if (i < per && first + i < a.N) {
+                const int lo = __ldg(a.offsets + first + i), hi = __ldg(a.offsets + first + i + 1);
+                if (lo < 0 || hi < lo || hi > a.rows_cap) set_status(a.status, LC_MOE_DEV_IDX_RANGE);
+                else rt[i] = (hi - lo + TOK - 1) / TOK;
             }
-            if (e < a.N) pre[e + 1] = run + n;
-            run += __shfl_sync(FULL, n, 31);
+            sum += rt[i];
+            some += rt[i] > 0;
         }
+        int sum_to = sum, some_to = some;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const int u = __shfl_up_sync(FULL, sum_to, o), v = __shfl_up_sync(FULL, some_to, o);
+            if (lane >= o) {
+                sum_to += u;
+                some_to += v;
+            }
+        }
+        if (lane == 31) {
+            part[warp] = sum_to;
+            part[W4_WARPS + warp] = some_to;
+        }
+        __syncthreads();
+        row_tiles = live = 0;
+#pragma unroll
+        for (int w = 0; w < W4_WARPS; ++w) {
+            if (w == warp) {
+                sum_to += row_tiles;
+                some_to += live;
+            }
+            row_tiles += part[w];
+            live += part[W4_WARPS + w];
+        }
+        int at = some_to - some, before = sum_to - sum;
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+            if (rt[i] > 0) {
+                pre[at] = before;
+                ids[at++] = static_cast<uint16_t>(first + i);
+                before += rt[i];
+            }
+        if (threadIdx.x == 0) pre[live] = row_tiles;
     }
     __syncthreads();
     const int tiles = a.m / (64 * HALVES), teams = W4_WARPS / a.split;
     const int team = warp / a.split, kw = warp % a.split;
     const int super = (tiles + teams - 1) / teams;  // items per row tile of an expert
-    const int64_t total = static_cast<int64_t>(pre[a.N]) * super;
     const int nk = a.k / 64;
     const int64_t mblk = a.m / 16;
 
+    // This CTA's items are blockIdx.x, blockIdx.x + gridDim.x, ... of row_tiles * super: (row tile,
+    // place among its `super`), and the live expert of the row tile.
+    struct Cursor {
+        int rt, place, e;
+    };
+    const int step_rt = gridDim.x / super, step_place = gridDim.x % super;
+    auto settle = [&](Cursor& c) {
+        while (c.e + 1 < live && pre[c.e + 1] <= c.rt) ++c.e;
+    };
+    auto advance = [&](Cursor& c) {
+        c.rt += step_rt;
+        c.place += step_place;
+        if (c.place >= super) {
+            c.place -= super;
+            ++c.rt;
+        }
+        settle(c);
+    };
+    auto begin = [&]() {
+        Cursor c{static_cast<int>(blockIdx.x) / super, static_cast<int>(blockIdx.x) % super, 0};
+        settle(c);
+        return c;
+    };
     struct Item {
         int row0, rows;  // first row, 1..TOK rows
         int e, tile;
     };
-    auto locate = [&](int64_t item) {
-        const int rt = static_cast<int>(item / super);
-        int lo = 0, hi = a.N - 1;
-        while (lo < hi) {
-            const int mid = (lo + hi + 1) >> 1;
-            if (pre[mid] <= rt) lo = mid;
-            else hi = mid - 1;
-        }
+    auto item_at = [&](const Cursor& c) {
         Item it;
-        it.e = lo;
-        it.tile = static_cast<int>(item - static_cast<int64_t>(rt) * super) * teams + team;
-        it.row0 = __ldg(a.offsets + lo) + (rt - pre[lo]) * TOK;
-        it.rows = min(TOK, __ldg(a.offsets + lo + 1) - it.row0);
+        it.e = ids[c.e];
+        it.tile = c.place * teams + team;
+        it.row0 = __ldg(a.offsets + it.e) + (c.rt - pre[c.e]) * TOK;
+        it.rows = min(TOK, __ldg(a.offsets + it.e + 1) - it.row0);
         return it;
     };
     // block b (16 weight rows) of the first half of a tile: SwiGLU takes two of the gate rows and two
@@ -274,21 +326,23 @@ __global__ void __launch_bounds__(W4_THREADS, 2) w4_kernel(const W4Args a) {
     const uint32_t ring = smem_u32(s_raw) + warp * STAGES * STAGE_BYTES + lane * 16;
     const uint32_t ring_sc = smem_u32(s_raw) + warp * STAGES * STAGE_BYTES + 2048 + t * 32 + g * 4;
     const uint32_t sc_step = 2048u / static_cast<uint32_t>(a.group);  // scale bytes per 64 columns
-    int64_t p_item = blockIdx.x;
+    Cursor pc = begin();
     int p_ks = nk;
     uint32_t p_slot = 0;
     const uint8_t *p_codes = nullptr, *p_scale = nullptr;
     auto produce = [&](auto half) {
         constexpr int H = decltype(half)::value;
         if (H == 0) {
-            while (p_ks >= nk && p_item < total) {  // next item in which this warp's team has a tile
-                const Item it = locate(p_item);
-                p_item += gridDim.x;
-                if (it.tile >= tiles) continue;
-                p_ks = kw;
-                p_codes = a.codes + (it.e * mblk + block_of(it.tile, 0)) * a.code_blk + kw * 512 + lane * 16;
-                // lane (g, t) fetches block t's scales of rows g and g + 8
-                p_scale = a.scale + (it.e * mblk + block_of(it.tile, t)) * a.scale_blk + g * 4;
+            while (p_ks >= nk && pc.rt < row_tiles) {  // next item in which this warp's team has a tile
+                const int tile = pc.place * teams + team;
+                if (tile < tiles) {
+                    const int64_t e = ids[pc.e];
+                    p_ks = kw;
+                    p_codes = a.codes + (e * mblk + block_of(tile, 0)) * a.code_blk + kw * 512 + lane * 16;
+                    // lane (g, t) fetches block t's scales of rows g and g + 8
+                    p_scale = a.scale + (e * mblk + block_of(tile, t)) * a.scale_blk + g * 4;
+                }
+                advance(pc);
             }
         }
         if (p_ks < nk) {
@@ -322,47 +376,54 @@ __global__ void __launch_bounds__(W4_THREADS, 2) w4_kernel(const W4Args a) {
 
     // ---- activations of the next step, in registers: rows g and g + 8 of the item. A row past the
     // item's last repeats the last (its column of the product is not stored).
-    auto row_ptr = [&](const Item& it, int n) {
-        return a.x + static_cast<int64_t>(it.row0 + min(g + 8 * n, it.rows - 1)) * a.k + (kw * 64 + 8 * t);
+    struct Rows {
+        const __nv_bfloat16* p;  // row g of the item, this lane's columns
+        int off[MAXNT];          // from there to rows g + 8 n, in elements
+    };
+    auto rows_of = [&](const Item& it) {
+        Rows r;
+        const int first = min(g, it.rows - 1);
+        r.p = a.x + static_cast<int64_t>(it.row0 + first) * a.k + (kw * 64 + 8 * t);
+#pragma unroll
+        for (int n = 0; n < MAXNT; ++n) r.off[n] = (min(g + 8 * n, it.rows - 1) - first) * a.k;
+        return r;
     };
     // H is written while the down product is already running: no read-only loads there
     auto load16 = [](const __nv_bfloat16* p) {
         return SWIGLU ? __ldg(reinterpret_cast<const uint4*>(p)) : *reinterpret_cast<const uint4*>(p);
     };
-    auto load_x = [&](uint4 (&v)[MAXNT][2], const __nv_bfloat16* p, int64_t to_row8, int rows) {
-        v[0][0] = load16(p);
-        v[0][1] = load16(p + 32);
-        if (MAXNT > 1 && rows > 8) {
-            v[MAXNT - 1][0] = load16(p + to_row8);
-            v[MAXNT - 1][1] = load16(p + to_row8 + 32);
-        }
+    auto load_x = [&](uint4 (&v)[MAXNT][2], const Rows& r, int rows) {
+#pragma unroll
+        for (int n = 0; n < MAXNT; ++n)
+            if (n == 0 || rows > 8 * n) {
+                v[n][0] = load16(r.p + r.off[n]);
+                v[n][1] = load16(r.p + r.off[n] + 32);
+            }
     };
     Item it{}, nx{};
-    const __nv_bfloat16 *xp = nullptr, *xnp = nullptr;
-    int64_t row8 = 0, row8n = 0;
+    Rows xr{}, xn{};
     uint4 xa[MAXNT][2], xb[MAXNT][2];
 #pragma unroll
     for (int n = 0; n < MAXNT; ++n) xa[n][0] = xa[n][1] = xb[n][0] = xb[n][1] = make_uint4(0, 0, 0, 0);
-    if (static_cast<int64_t>(blockIdx.x) < total) {
-        nx = locate(blockIdx.x);
-        xnp = row_ptr(nx, 0);
-        if (MAXNT > 1) row8n = row_ptr(nx, 1) - xnp;
-        load_x(xa, xnp, row8n, nx.rows);
+    Cursor c = begin();
+    if (c.rt < row_tiles) {
+        nx = item_at(c);
+        xn = rows_of(nx);
+        load_x(xa, xn, nx.rows);
     }
     uint32_t slot = 0;
     int buf = 0;
     const uint8_t* my_ring = s_raw + warp * STAGES * STAGE_BYTES;
     const int steps = (nk - kw + a.split - 1) / a.split;
     const int x_step = a.split * 64;
-    for (int64_t item = blockIdx.x; item < total; item += gridDim.x) {
+    while (c.rt < row_tiles) {
         it = nx;
-        xp = xnp;
-        row8 = row8n;
-        const bool more = item + gridDim.x < total;
+        xr = xn;
+        advance(c);
+        const bool more = c.rt < row_tiles;
         if (more) {
-            nx = locate(item + gridDim.x);
-            xnp = row_ptr(nx, 0);
-            if (MAXNT > 1) row8n = row_ptr(nx, 1) - xnp;
+            nx = item_at(c);
+            xn = rows_of(nx);
         }
         const bool mine = it.tile < tiles;
         float acc[4 * HALVES][MAXNT][4];
@@ -377,9 +438,9 @@ __global__ void __launch_bounds__(W4_THREADS, 2) w4_kernel(const W4Args a) {
             // one step on the activations `v`, while those of the next step (of this item or the next) load into `w`
             auto step = [&](auto nt, uint4 (&v)[MAXNT][2], uint4 (&w)[MAXNT][2]) {
                 constexpr int NT = decltype(nt)::value;
-                xp += x_step;
-                if (--left) load_x(w, xp, row8, it.rows);
-                else if (more) load_x(w, xnp, row8n, nx.rows);
+                xr.p += x_step;
+                if (--left) load_x(w, xr, it.rows);
+                else if (more) load_x(w, xn, nx.rows);
                 auto half = [&](auto h, auto ahead) {
                     cp_async_wait<STAGES - 2>();
                     __syncwarp();  // the stage is visible, and the slot before it has been read by every lane
@@ -408,7 +469,7 @@ __global__ void __launch_bounds__(W4_THREADS, 2) w4_kernel(const W4Args a) {
             if (MAXNT > 1 && it.rows > 8) run(Int<MAXNT>());
             else run(Int<1>());
         } else if (more) {
-            load_x(xa, xnp, row8n, nx.rows);
+            load_x(xa, xn, nx.rows);
         }
         // join the team's partial sums, 8 rows x 64 weight rows at a time (two buffers: one barrier each)
 #pragma unroll
@@ -426,19 +487,24 @@ __global__ void __launch_bounds__(W4_THREADS, 2) w4_kernel(const W4Args a) {
             }
             __syncthreads();
             if (mine) {
-                constexpr int FEAT = SWIGLU ? 32 : 64;
+                // two neighbouring features a thread
+                constexpr int PAIRS = SWIGLU ? 16 : 32;
                 const float* s = r + team * a.split * RED_WARP;
-                for (int i = kw * 32 + lane; i < 8 * FEAT; i += a.split * 32) {
-                    const int row = i / FEAT, f = i % FEAT;
-                    if (8 * n + row < it.rows) {
-                        float p = 0.0f, q = 0.0f;
-                        for (int k = 0; k < a.split; ++k) {
-                            p += s[k * RED_WARP + row * RED + f];
-                            if (SWIGLU) q += s[k * RED_WARP + row * RED + 32 + f];
+                __nv_bfloat16* dst = a.out + static_cast<int64_t>(it.row0 + 8 * n) * a.n_out + (it.tile * HALVES + hf) * (2 * PAIRS);
+                const int rows = min(8, it.rows - 8 * n);
+                for (int i = kw * 32 + lane; i < rows * PAIRS; i += a.split * 32) {
+                    const int row = i / PAIRS, f = 2 * (i % PAIRS);
+                    float2 p = make_float2(0.0f, 0.0f), q = p;
+                    for (int k = 0; k < a.split; ++k) {
+                        const float2 u = *reinterpret_cast<const float2*>(s + k * RED_WARP + row * RED + f);
+                        p.x += u.x, p.y += u.y;
+                        if (SWIGLU) {
+                            const float2 v = *reinterpret_cast<const float2*>(s + k * RED_WARP + row * RED + 32 + f);
+                            q.x += v.x, q.y += v.y;
                         }
-                        a.out[static_cast<int64_t>(it.row0 + 8 * n + row) * a.n_out + (it.tile * HALVES + hf) * FEAT + f] =
-                            __float2bfloat16_rn(SWIGLU ? silu_mul(p, q) : p);
                     }
+                    if (SWIGLU) p = make_float2(silu_mul(p.x, q.x), silu_mul(p.y, q.y));
+                    *reinterpret_cast<uint32_t*>(dst + static_cast<int64_t>(row) * a.n_out + f) = pack_bf16x2(p.x, p.y);
                 }
             }
             buf ^= 1;
@@ -454,17 +520,17 @@ cudaError_t launch_w4_t(const W4Args& a, cudaStream_t st) {
     static PerDeviceOnce setup;
     const cudaError_t e = setup.run([](int) {
         return cudaFuncSetAttribute(w4_kernel<SWIGLU, G32, HALVES, MAXNT>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                    static_cast<int>(RING_BYTES + RED_BYTES + 2049 * 4));
+                                    static_cast<int>(w4_smem(2048)));
     });
     if (e != cudaSuccess) return e;
-    const size_t smem = RING_BYTES + RED_BYTES + (static_cast<size_t>(a.N) + 1) * 4;
+    const size_t smem = w4_smem(a.N);
     // The down product is launched while the gate/up product still runs: its CTAs fetch their first
     // weights as SMs become free and wait for the other kernel before they read H.
     cudaLaunchAttribute attr;
     attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attr.val.programmaticStreamSerializationAllowed = 1;
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(di->sm_count * 2);
+    cfg.gridDim = dim3(di->sm_count * W4_CTAS);
     cfg.blockDim = dim3(W4_THREADS);
     cfg.dynamicSmemBytes = smem;
     cfg.stream = st;
@@ -488,16 +554,20 @@ int split_of(const W4Args& a, int tile_rows, int tok) {
     return split;
 }
 
-template <bool SWIGLU>
-cudaError_t launch_w4(W4Args a, bool few_rows, cudaStream_t st) {
+template <bool SWIGLU, int HALVES, int MAXNT>
+cudaError_t launch_w4_n(W4Args a, cudaStream_t st) {
     a.code_blk = static_cast<int64_t>(a.k / 64) * 512;
     a.scale_blk = static_cast<int64_t>(a.k / a.group) * 32;
     a.code_up = SWIGLU ? a.m / 32 * a.code_blk : 2 * a.code_blk;
-    const bool wide = few_rows && a.m % 128 == 0;
-    a.split = split_of(a, wide ? 128 : 64, wide ? 8 : 16);
-    if (wide)
-        return a.group == 32 ? launch_w4_t<SWIGLU, true, 2, 1>(a, st) : launch_w4_t<SWIGLU, false, 2, 1>(a, st);
-    return a.group == 32 ? launch_w4_t<SWIGLU, true, 1, 2>(a, st) : launch_w4_t<SWIGLU, false, 1, 2>(a, st);
+    a.split = split_of(a, 64 * HALVES, 8 * MAXNT);
+    return a.group == 32 ? launch_w4_t<SWIGLU, true, HALVES, MAXNT>(a, st) : launch_w4_t<SWIGLU, false, HALVES, MAXNT>(a, st);
+}
+
+// The tile by the rows an expert can have on average (rows_cap / N; zero experts take some of them).
+template <bool SWIGLU>
+cudaError_t launch_w4(const W4Args& a, cudaStream_t st) {
+    if (a.rows_cap < static_cast<int64_t>(8) * a.N && a.m % 128 == 0) return launch_w4_n<SWIGLU, 2, 1>(a, st);
+    return launch_w4_n<SWIGLU, 1, 2>(a, st);
 }
 
 }  // namespace
@@ -521,7 +591,7 @@ cudaError_t launch_swiglu_w4(const void* x_perm, int64_t rows_cap, const int32_t
     W4Args a{offsets, static_cast<const __nv_bfloat16*>(x_perm), static_cast<const uint8_t*>(w13q),
              static_cast<const uint8_t*>(w13_scale), static_cast<__nv_bfloat16*>(h), status, rows_cap,
              N, d, 2 * I, I, group, 0, 0, 0, 0};
-    return launch_w4<true>(a, rows_cap < static_cast<int64_t>(8) * N, st);
+    return launch_w4<true>(a, st);
 }
 
 cudaError_t launch_down_w4(const void* h, int64_t rows_cap, const int32_t* offsets, int N, const void* w2q,
@@ -530,7 +600,7 @@ cudaError_t launch_down_w4(const void* h, int64_t rows_cap, const int32_t* offse
     W4Args a{offsets, static_cast<const __nv_bfloat16*>(h), static_cast<const uint8_t*>(w2q),
              static_cast<const uint8_t*>(w2_scale), static_cast<__nv_bfloat16*>(y), status, rows_cap,
              N, I, d, d, group, 0, 0, 0, 0};
-    return launch_w4<false>(a, rows_cap < static_cast<int64_t>(8) * N, st);
+    return launch_w4<false>(a, st);
 }
 
 }  // namespace lcmoe
