@@ -8,6 +8,7 @@ The library is loaded on first use. If it has not been built, or the device is n
 from __future__ import annotations
 
 import ctypes
+import functools
 import pathlib
 import threading
 
@@ -585,8 +586,16 @@ def _on_stream(make, stream, *args, **kw):
         return make(*args, **kw)
 
 
-def _empty(stream, device, dtype, *shape):
+def _empty(stream, device, dtype, shape):
+    if stream is None:
+        return torch.empty(shape, dtype=dtype, device=device)
     return _on_stream(torch.empty, stream, shape, dtype=dtype, device=device)
+
+
+@functools.lru_cache(maxsize=1024)
+def _shape_arg(T, d, N, Z, K, I):
+    """A shape argument (read only), made once for each shape."""
+    return ctypes.byref(Shape(T, d, N, Z, K, I))
 
 
 def _dims_of(t, n, name):
@@ -595,10 +604,12 @@ def _dims_of(t, n, name):
     return tuple(t.shape)
 
 
-def _gate_opts(score, groups, top_groups, group_rank, renorm, scale) -> GateOpts:
+@functools.lru_cache(maxsize=1024)
+def _gate_opts(score, groups, top_groups, group_rank, renorm, scale):
+    """An options argument (read only), made once for each set of options."""
     if score not in SCORES:
         raise ValueError(f"score: expected one of {sorted(SCORES)}, got {score!r}")
-    return GateOpts(SCORES[score], groups, top_groups, group_rank, int(bool(renorm)), scale)
+    return ctypes.byref(GateOpts(SCORES[score], groups, top_groups, group_rank, int(bool(renorm)), scale))
 
 
 def lc_moe_gate(logits, bias, K: int, N: int, score: str = "softmax", groups: int = 1, top_groups: int = 1,
@@ -623,14 +634,14 @@ def lc_moe_gate(logits, bias, K: int, N: int, score: str = "softmax", groups: in
     if gate is not None:
         _expect(gate, torch.float32, (T, K), dev, "gate")
     if idx is None:
-        idx = _empty(stream, dev, torch.int32, T, K)
+        idx = _empty(stream, dev, torch.int32, (T, K))
     if gate is None:
-        gate = _empty(stream, dev, torch.float32, T, K)
+        gate = _empty(stream, dev, torch.float32, (T, K))
     if ws is None:
         ws = _on_stream(_status_ws, stream, dev)
     _expect_ws(ws, dev)
-    s = Shape(T, 64, N, E - N, K, 64)
-    _check(_lib().lc_moe_gate(ctypes.byref(s), ctypes.byref(o), logits.data_ptr(), kind, _addr(bias), idx.data_ptr(),
+    s = _shape_arg(T, 64, N, E - N, K, 64)
+    _check(_lib().lc_moe_gate(s, o, logits.data_ptr(), kind, _addr(bias), idx.data_ptr(),
                               gate.data_ptr(), _addr(counts), ws.data_ptr(), ws.nbytes, _raw_stream(stream, dev)),
            "lc_moe_gate")
     return idx, gate
@@ -652,12 +663,12 @@ def lc_moe_gate_backward(logits, idx, dgate, score: str = "softmax", renorm: boo
     if dlogits is not None:
         _expect(dlogits, logits.dtype, (T, E), dev, "dlogits")
     if dlogits is None:
-        dlogits = _empty(stream, dev, logits.dtype, T, E)
+        dlogits = _empty(stream, dev, logits.dtype, (T, E))
     if ws is None:
         ws = _on_stream(_status_ws, stream, dev)
     _expect_ws(ws, dev)
-    s = Shape(T, 64, E, 0, K, 64)
-    _check(_lib().lc_moe_gate_backward(ctypes.byref(s), ctypes.byref(o), logits.data_ptr(), kind, idx.data_ptr(),
+    s = _shape_arg(T, 64, E, 0, K, 64)
+    _check(_lib().lc_moe_gate_backward(s, o, logits.data_ptr(), kind, idx.data_ptr(),
                                        dgate.data_ptr(), dlogits.data_ptr(), ws.data_ptr(), ws.nbytes,
                                        _raw_stream(stream, dev)), "lc_moe_gate_backward")
     return dlogits
@@ -685,14 +696,14 @@ def lc_moe_combine_backward(dout, x, y, gate, pair_row, dy=None, dgate=None, dx=
     if dy is None:
         dy = _on_stream(torch.zeros, stream, rows, d, dtype=torch.bfloat16, device=dev)
     if dgate is None:
-        dgate = _empty(stream, dev, torch.float32, T, K)
+        dgate = _empty(stream, dev, torch.float32, (T, K))
     if dx is None:
-        dx = _empty(stream, dev, torch.bfloat16, T, d)
+        dx = _empty(stream, dev, torch.bfloat16, (T, d))
     if ws is None:
         ws = _on_stream(_status_ws, stream, dev)
     _expect_ws(ws, dev)
-    s = Shape(T, d, 1, K, K, 64)
-    _check(_lib().lc_moe_combine_backward(ctypes.byref(s), dout.data_ptr(), x.data_ptr(), y.data_ptr(), rows,
+    s = _shape_arg(T, d, 1, K, K, 64)
+    _check(_lib().lc_moe_combine_backward(s, dout.data_ptr(), x.data_ptr(), y.data_ptr(), rows,
                                           gate.data_ptr(), pair_row.data_ptr(), dy.data_ptr(), dgate.data_ptr(),
                                           dx.data_ptr(), ws.data_ptr(), ws.nbytes, _raw_stream(stream, dev)),
            "lc_moe_combine_backward")
@@ -715,9 +726,9 @@ def lc_moe_quantize_w4(src, group: int = 64, codes=None, scale=None, stream=None
     if scale is not None:
         _expect(scale, torch.bfloat16, (*lead, rows // 16, cols // group, 16), dev, "scale")
     if codes is None:
-        codes = _empty(stream, dev, torch.uint8, *lead, rows, cols // 2)
+        codes = _empty(stream, dev, torch.uint8, (*lead, rows, cols // 2))
     if scale is None:
-        scale = _empty(stream, dev, torch.bfloat16, *lead, rows // 16, cols // group, 16)
+        scale = _empty(stream, dev, torch.bfloat16, (*lead, rows // 16, cols // group, 16))
     if src.numel():
         _check(_lib().lc_moe_quantize_w4(src.data_ptr(), src.numel() // cols, cols, group, codes.data_ptr(),
                                          scale.data_ptr(), _raw_stream(stream, dev)), "lc_moe_quantize_w4")
@@ -755,14 +766,14 @@ def lc_moe_expert_ffn_w4(x_perm, offsets, w13q, w13_scale, w2q, w2_scale, T: int
     if y is not None:
         _expect(y, torch.bfloat16, (rows, d), dev, "y")
     if h is None:
-        h = _empty(stream, dev, torch.bfloat16, rows, I)
+        h = _empty(stream, dev, torch.bfloat16, (rows, I))
     if y is None:
-        y = _empty(stream, dev, torch.bfloat16, rows, d)
+        y = _empty(stream, dev, torch.bfloat16, (rows, d))
     if ws is None:
         ws = _on_stream(_status_ws, stream, dev)
     _expect_ws(ws, dev)
-    s = Shape(T, d, N, max(0, K - N), K, I)
-    _check(_lib().lc_moe_expert_ffn_w4(ctypes.byref(s), x_perm.data_ptr(), offsets.data_ptr(), w13q.data_ptr(),
+    s = _shape_arg(T, d, N, max(0, K - N), K, I)
+    _check(_lib().lc_moe_expert_ffn_w4(s, x_perm.data_ptr(), offsets.data_ptr(), w13q.data_ptr(),
                                        w13_scale.data_ptr(), w2q.data_ptr(), w2_scale.data_ptr(), group, h.data_ptr(),
                                        y.data_ptr(), ws.data_ptr(), ws.nbytes, _raw_stream(stream, dev)),
            "lc_moe_expert_ffn_w4")
@@ -795,13 +806,13 @@ def lc_moe_forward_w4(x, wr, bias, w13q, w13_scale, w2q, w2_scale, K: int, opts:
         _expect(gate, torch.float32, (T, K), dev, "gate")
     if counts is not None:
         _expect(counts, torch.int32, (E,), dev, "counts")
-    s = Shape(T, d, N, E - N, K, I)
+    s = _shape_arg(T, d, N, E - N, K, I)
     if out is None:
-        out = _empty(stream, dev, torch.bfloat16, T, d)
+        out = _empty(stream, dev, torch.bfloat16, (T, d))
     if ws is None:
-        ws = _on_stream(new_workspace, stream, s, OP_FORWARD_W4, dev)
+        ws = _on_stream(new_workspace, stream, Shape(T, d, N, E - N, K, I), OP_FORWARD_W4, dev)
     _expect_ws(ws, dev)
-    _check(_lib().lc_moe_forward_w4(ctypes.byref(s), None if o is None else ctypes.byref(o), x.data_ptr(), wr.data_ptr(),
+    _check(_lib().lc_moe_forward_w4(s, o, x.data_ptr(), wr.data_ptr(),
                                     _addr(bias), w13q.data_ptr(), w13_scale.data_ptr(), w2q.data_ptr(),
                                     w2_scale.data_ptr(), group, out.data_ptr(), _addr(idx), _addr(gate), _addr(counts),
                                     ws.data_ptr(), ws.nbytes, _raw_stream(stream, dev)), "lc_moe_forward_w4")

@@ -542,14 +542,14 @@ cudaError_t launch_w4_t(const W4Args& a, cudaStream_t st) {
 }
 
 // Warps on a tile's reduction. Fewer warps mean fewer sums to join, but also fewer and longer items:
-// a split that leaves a warp 8 steps of 64 columns, raised while there are fewer than 8 items an SM
-// (one token over 8 experts, down product: 22 us with 4 warps on a tile, SPLIT8 with 8).
+// a split that leaves a warp 16 steps of 64 columns, raised while there are fewer than 8 items an SM
+// (one token over 8 experts, down product: 22 us with 4 warps on a tile, 20 with 8).
 int split_of(const W4Args& a, int tile_rows, int tok) {
     const int64_t tiles = a.m / tile_rows, row_tiles = (a.rows_cap < a.N ? a.rows_cap : a.N) + a.rows_cap / tok;
     const int steps = a.k / 64;
     int split = 1;
     while (split < W4_WARPS && split * 2 <= steps &&
-           (steps / split >= 16 || row_tiles * ((tiles * split + W4_WARPS - 1) / W4_WARPS) < 8 * 148))
+           (steps / split >= 32 || row_tiles * ((tiles * split + W4_WARPS - 1) / W4_WARPS) < 8 * 148))
         split *= 2;
     return split;
 }
