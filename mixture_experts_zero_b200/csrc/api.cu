@@ -577,6 +577,7 @@ int lc_moe_combine_backward(const lc_moe_shape* s, const void* dout, const void*
     for (const void* p : {dout, x, y, static_cast<const void*>(dy), static_cast<const void*>(dx),
                           static_cast<const void*>(ws)})
         if (p && !aligned16(p)) return LC_MOE_ERR_MISALIGNED;
+    if ((y && dy == y) || dx == x || dx == dout) return LC_MOE_ERR_INVALID_ARG;  // not in place
     LC_TRY(device_ok());
     LC_CUDA(launch_combine_backward(dout, x, y, y_rows, gate, pair_row, s->T, s->d, s->K, dy, dgate, dx,
                                     at<uint32_t>(ws, 0), static_cast<cudaStream_t>(stream)));

@@ -206,9 +206,9 @@ __device__ __noinline__ int pick64(double* key, int E, int K, uint32_t kept, int
 
 // Error bounds of the fp32 keys. u = 2^-23.
 //   softmax: __expf is within 2 + 1.2 x steps at -x = z - m, whose rounding adds x / 2; the sum of E
-//   terms averages that over the softmax (x is ln E <= 7.7 on average at most: 15 steps), its 29
-//   additions in sequence add 15, quotient, product and sum 2: s is within (36 + 1.7 x) u s, which
-//   is at most 36 u / S for any x >= 0, and 2^-15 s for every x <= 88.
+//   terms averages that over the softmax (x is ln E <= 7.7 on average at most: 15 u), its up to 69
+//   additions in sequence add 35 u, quotient, product and key 4 u: s is within (56 + 1.7 x) u s,
+//   which is at most 56 u / S for any x >= 0, and 2^-15 s for every x <= 88.
 //   sigmoid: (6 + 1.2 max(-z, 0)) u s, at most 7 u for any z, and 2^-16 s for every z >= -88.
 //   Scores below e^-87 count as 0 (1e-37 covers them); key = s + b adds u |key|.
 constexpr float U23 = 1.1920929e-07f;
@@ -258,8 +258,8 @@ __global__ void __launch_bounds__(VPL <= 32 ? 256 : 128, gate_ctas(VPL))
     }
     const int stride = gridDim.x * warps;
     auto in = [&](int j) { return FILLED || lane + 32 * j < E; };  // whether place j of this lane is an expert
-    for (int t = blockIdx.x * warps + warp; t < T; t += stride) {
-        const LT* zt = logits + static_cast<int64_t>(t) * E;
+    for (int64_t t = blockIdx.x * warps + warp; t < T; t += stride) {
+        const LT* zt = logits + t * E;
         float v[VPL];
 #pragma unroll
         for (int j = 0; j < VPL; ++j) v[j] = in(j) ? load_logit(zt + lane + 32 * j) : NEG_INF;
@@ -317,7 +317,7 @@ __global__ void __launch_bounds__(VPL <= 32 ? 256 : 128, gate_ctas(VPL))
                 if (sigmoid ? k < -700.0f : m0 - k > 700.0f) return __int_as_float(0x7f800000);
                 return 1e-13f + (sigmoid ? 1e-15f * __expf(fminf(k, 80.0f)) : 0.0f);
             }
-            const float rel = (sigmoid ? 0x1p-16f : 0x1p-15f) * (k - bmin), all = (sigmoid ? 7.0f : 36.0f * inv_S) * U23;
+            const float rel = (sigmoid ? 0x1p-16f : 0x1p-15f) * (k - bmin), all = (sigmoid ? 7.0f : 56.0f * inv_S) * U23;
             return fminf(rel, all) + U23 * fabsf(k) + 1e-37f;
         };
         // kept: the groups that stay (0: a key or a group's score is NaN)
@@ -424,7 +424,7 @@ __global__ void __launch_bounds__(VPL <= 32 ? 256 : 128, gate_ctas(VPL))
                 } else {
                     const float s = __expf(z - m0) * inv_S;
                     k = s + b;
-                    err = s * (36.0f + 1.7f * fminf(m0 - z, 88.0f)) * U23 + U23 * fabsf(k) + 1e-37f;
+                    err = s * (56.0f + 1.7f * fminf(m0 - z, 88.0f)) * U23 + U23 * fabsf(k) + 1e-37f;
                 }
             }
             int rank = 0;
@@ -481,7 +481,7 @@ __global__ void __launch_bounds__(VPL <= 32 ? 256 : 128, gate_ctas(VPL))
         else if (sigmoid) g = sigmoid32(z);
         else g = expf(z - m0) * inv_S;
         if (lane < K) {
-            const int64_t at = static_cast<int64_t>(t) * K + lane;
+            const int64_t at = t * K + lane;
             idx[at] = my_idx;
             gate[at] = bad ? __int_as_float(0x7fc00000) : o.scale * g;
             if (counts) atomicAdd(&s_hist[my_idx], 1);
@@ -537,12 +537,13 @@ __global__ void __launch_bounds__(GATE_THREADS)
     gate_backward_kernel(const LT* __restrict__ logits, const int32_t* __restrict__ idx,
                          const float* __restrict__ dgate, int T, int E, int K, lc_moe_gate_opts o,
                          LT* __restrict__ dlogits, uint32_t* __restrict__ status) {
-    const int t = blockIdx.x * (GATE_THREADS / 32) + (threadIdx.x >> 5), lane = threadIdx.x & 31;
+    const int64_t t = static_cast<int64_t>(blockIdx.x) * (GATE_THREADS / 32) + (threadIdx.x >> 5);
+    const int lane = threadIdx.x & 31;
     if (t >= T) return;
     const bool sigmoid = o.score == LC_MOE_SCORE_SIGMOID;
     const float NEG_INF = __int_as_float(0xff800000);
-    const LT* zt = logits + static_cast<int64_t>(t) * E;
-    LT* out = dlogits + static_cast<int64_t>(t) * E;
+    const LT* zt = logits + t * E;
+    LT* out = dlogits + t * E;
     constexpr int NV = V / W;
     float e[V > 0 ? V : 1];
     if (V > 0) {
@@ -557,13 +558,13 @@ __global__ void __launch_bounds__(GATE_THREADS)
     int i = -1;
     float z = NEG_INF, dg = 0.0f;
     if (lane < K) {
-        i = idx[static_cast<int64_t>(t) * K + lane];
+        i = idx[t * K + lane];
         if (i < 0 || i >= E) {
             set_status(status, LC_MOE_DEV_IDX_RANGE);
             i = -1;
         } else {
             z = load_logit(zt + i);
-            dg = o.scale * dgate[static_cast<int64_t>(t) * K + lane];
+            dg = o.scale * dgate[t * K + lane];
         }
     }
     float mine;  // dz of the chosen logit through its own score
@@ -646,7 +647,7 @@ cudaError_t launch_gate_f(const LT* logits, const float* bias, int T, int E, int
     int row_len = E > 32 ? E : 32;
     if (o.top_groups < o.groups && (E + o.groups * pad + 1) / 2 > row_len) row_len = (E + o.groups * pad + 1) / 2;
     const size_t smem = static_cast<size_t>(warps) * row_len * 8 + (counts ? static_cast<size_t>(E) * 4 : 0);
-    int blocks = (T + warps - 1) / warps;
+    int blocks = (T - 1) / warps + 1;
     if (blocks > di->sm_count * gate_ctas(VPL)) blocks = di->sm_count * gate_ctas(VPL);  // one wave
     gate_kernel<LT, VPL, FILLED><<<blocks, warps * 32, smem, st>>>(logits, bias, T, E, K, o, team, pad, row_len, idx, gate,
                                                                  counts, status);

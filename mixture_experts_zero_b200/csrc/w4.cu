@@ -378,14 +378,14 @@ __global__ void __launch_bounds__(W4_THREADS, W4_CTAS) w4_kernel(const W4Args a)
     // item's last repeats the last (its column of the product is not stored).
     struct Rows {
         const __nv_bfloat16* p;  // row g of the item, this lane's columns
-        int off[MAXNT];          // from there to rows g + 8 n, in elements
+        int64_t off[MAXNT];      // from there to rows g + 8 n, in elements
     };
     auto rows_of = [&](const Item& it) {
         Rows r;
         const int first = min(g, it.rows - 1);
         r.p = a.x + static_cast<int64_t>(it.row0 + first) * a.k + (kw * 64 + 8 * t);
 #pragma unroll
-        for (int n = 0; n < MAXNT; ++n) r.off[n] = (min(g + 8 * n, it.rows - 1) - first) * a.k;
+        for (int n = 0; n < MAXNT; ++n) r.off[n] = static_cast<int64_t>(min(g + 8 * n, it.rows - 1) - first) * a.k;
         return r;
     };
     // H is written while the down product is already running: no read-only loads there

@@ -86,6 +86,10 @@ def test_combine_backward_arguments(lib):
     for k in ("dout", "x", "y", "g", "pr", "dy", "dg", "dx", "ws"):
         assert call(**{k: None}) == INV
     assert call(rows=-1) == INV
+    a, b, c = (ctypes.c_void_p(v) for v in (4096, 8192, 12288))
+    assert call(y=a, dy=a, dx=b) == INV         # in place
+    assert call(y=a, dy=b, x=c, dx=c) == INV
+    assert call(y=a, dy=b, dout=c, dx=c) == INV
     assert call(n=0) == SMALL
     for k in ("dout", "x", "y", "dy", "dx", "ws"):
         assert call(**{k: ctypes.c_void_p(264)}) == MIS

@@ -79,6 +79,16 @@ def test_many_tokens(cuda_device, score):
 
 
 @pytest.mark.parametrize("score", ["softmax", "sigmoid"])
+def test_many_experts_with_crowded_keys(cuda_device, score):
+    """2048 experts whose scores the biases level out, so that neighbours in the order are close."""
+    z = logits_of(400, 2048, 6, False, std=0.5)
+    b = -torch.from_numpy(R.scores(f64(z[:1]), score)[0].astype(np.float32)).cuda()
+    check_gate(z, b, 32, 1024, score)
+    check_gate(z[:50], b, 32, 1024, score, groups=16, top=5, rank=2)
+    check_gate(z[:1], b, 32, 1024, score)      # every key is a rounding error
+
+
+@pytest.mark.parametrize("score", ["softmax", "sigmoid"])
 def test_keys_that_fp32_cannot_tell_apart(cuda_device, score):
     """Neighbouring fp32 logits and biases that nearly undo their differences."""
     rng = np.random.default_rng(3)
