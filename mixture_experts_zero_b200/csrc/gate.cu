@@ -97,30 +97,69 @@ __device__ __forceinline__ float redux_min(float v) {
     return r;
 }
 
-// The 32 lanes' values in descending order over the lanes (bitonic network).
-__device__ __forceinline__ float sort_descending(float v) {
+// Which lanes keep the larger value in the 15 steps of a bitonic network that sorts in descending
+// order: bit s for step s.
+__device__ __forceinline__ uint32_t sort_directions() {
     const uint32_t lane = threadIdx.x & 31;
+    uint32_t dir = 0, s = 0;
 #pragma unroll
     for (uint32_t k = 2; k <= 32; k *= 2)
 #pragma unroll
-        for (uint32_t j = k / 2; j; j /= 2) {
+        for (uint32_t j = k / 2; j; j /= 2) dir |= (~(lane / j ^ lane / k) & 1u) << s++;
+    return dir;
+}
+// The 32 lanes' values in descending order over the lanes.
+__device__ __forceinline__ float sort_descending(float v, uint32_t dir) {
+    int s = 0;
+#pragma unroll
+    for (int k = 2; k <= 32; k *= 2)
+#pragma unroll
+        for (int j = k / 2; j; j /= 2, ++s) {
             const float w = __shfl_xor_sync(FULL, v, j);
-            // the larger value to the lane where bits j and k of the lane's number agree
-            const bool larger = ((lane / j ^ lane / k) & 1u) == 0;
-            v = larger ? fmaxf(v, w) : fminf(v, w);
+            v = dir & (1u << s) ? fmaxf(v, w) : fminf(v, w);
         }
     return v;
+}
+
+// largest of a lane's values (three operands an instruction)
+template <int N>
+__device__ __forceinline__ float largest(const float (&v)[N]) {
+    float m = v[0];
+#pragma unroll
+    for (int j = 1; j < N; j += 2) {
+        if (j + 1 < N) asm("max.f32 %0, %1, %2, %3;" : "=f"(m) : "f"(m), "f"(v[j]), "f"(v[j + 1 < N ? j + 1 : j]));
+        else m = fmaxf(m, v[j]);
+    }
+    return m;
+}
+
+// a >= b, a > b as 1 or 0: sums and bit patterns of such tests then run on the floating-point pipe,
+// which has room where the comparisons fill the other
+__device__ __forceinline__ float is_ge(float a, float b) {
+    float r;
+    asm("set.ge.f32.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
+    return r;
+}
+__device__ __forceinline__ float is_gt(float a, float b) {
+    float r;
+    asm("set.gt.f32.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
+    return r;
 }
 
 // 64-bit softmax denominator of a row with maximum m (1 for a row of -inf, whose scores are 0).
 template <class LT>
 __device__ __noinline__ double softmax_sum64(const LT* zt, int E, float m) {
-    double part = 0.0;
-    for (int i = threadIdx.x & 31; i < E; i += 32) {
-        const float z = load_logit(zt + i);
-        part += z == m && m < 0.0f && isinf(m) ? 0.0 : exp(static_cast<double>(z) - m);
+    // four exponentials at a time: one alone is a long chain of dependent operations
+    double part[4] = {};
+    const bool none = m < 0.0f && isinf(m);
+    for (int base = threadIdx.x & 31; base < E && !none; base += 128) {
+        float z[4];
+#pragma unroll
+        for (int q = 0; q < 4; ++q) z[q] = base + 32 * q < E ? load_logit(zt + base + 32 * q) : __int_as_float(0xff800000);
+#pragma unroll
+        for (int q = 0; q < 4; ++q) part[q] += exp(static_cast<double>(z[q]) - m);
     }
-    const double S = warp_sum(part);
+    const double S = warp_sum((part[0] + part[1]) + (part[2] + part[3]));
     return S == 0.0 ? 1.0 : S;
 }
 
@@ -136,11 +175,19 @@ __device__ __noinline__ bool keys64(const LT* zt, const float* bias, int E, bool
     const double S = sigmoid ? 1.0 : softmax_sum64(zt, E, m);
     bool nan = false;
     __syncwarp();
-    for (int i = lane; i < E; i += 32) {
-        const double s = score64(load_logit(zt + i), m, S, sigmoid);
-        const double k = bias ? s + static_cast<double>(__ldg(bias + i)) : s;
-        nan |= k != k;
-        key[i] = k;
+    for (int base = lane; base < E; base += 128) {
+        double k[4];
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+            const int i = min(base + 32 * q, E - 1);
+            k[q] = score64(load_logit(zt + i), m, S, sigmoid) + (bias ? static_cast<double>(__ldg(bias + i)) : 0.0);
+        }
+#pragma unroll
+        for (int q = 0; q < 4; ++q)
+            if (base + 32 * q < E) {
+                nan |= k[q] != k[q];
+                key[base + 32 * q] = k[q];
+            }
     }
     __syncwarp();
     return __any_sync(FULL, nan);
@@ -206,10 +253,12 @@ __device__ __noinline__ int pick64(double* key, int E, int K, uint32_t kept, int
 
 // Error bounds of the fp32 keys. u = 2^-23.
 //   softmax: __expf is within 2 + 1.2 x steps at -x = z - m, whose rounding adds x / 2; the sum of E
-//   terms averages that over the softmax (x is ln E <= 7.7 on average at most: 15 u), its up to 69
-//   additions in sequence add 35 u, quotient, product and key 4 u: s is within (56 + 1.7 x) u s,
-//   which is at most 56 u / S for any x >= 0, and 2^-15 s for every x <= 88.
-//   sigmoid: (6 + 1.2 max(-z, 0)) u s, at most 7 u for any z, and 2^-16 s for every z >= -88.
+//   terms averages that over the softmax (x is ln E <= 7.7 on average at most: 15 u), its additions
+//   (up to 16 in sequence in each of four chains, 2 to join them, 5 over the lanes) add 12 u, quotient,
+//   product and key 4 u: s is within (33 + 1.7 x) u s, which is at most 33 u / S for any x >= 0, and
+//   2^-15 s for every x <= 88.
+//   sigmoid: __expf(-z) is within 2 + 1.2 |z| steps and counts for 1 - s of the quotient, whose sum and
+//   quotient add 3 u: (3.5 + (1 - s) (2 + 1.2 |z|)) u s, at most 7 u for any z, and 2^-16 s for z >= -88.
 //   Scores below e^-87 count as 0 (1e-37 covers them); key = s + b adds u |key|.
 constexpr float U23 = 1.1920929e-07f;
 
@@ -257,6 +306,7 @@ __global__ void __launch_bounds__(VPL <= 32 ? 256 : 128, gate_ctas(VPL))
         bmin = redux_min(bmin);
     }
     const int stride = gridDim.x * warps;
+    const uint32_t dir = sort_directions();
     auto in = [&](int j) { return FILLED || lane + 32 * j < E; };  // whether place j of this lane is an expert
     for (int64_t t = blockIdx.x * warps + warp; t < T; t += stride) {
         const LT* zt = logits + t * E;
@@ -266,9 +316,7 @@ __global__ void __launch_bounds__(VPL <= 32 ? 256 : 128, gate_ctas(VPL))
         float m = NEG_INF, S = 1.0f, inv_S = 1.0f;
         bool nan = false;
         if (!sigmoid) {
-#pragma unroll
-            for (int j = 0; j < VPL; ++j) m = fmaxf(m, v[j]);
-            m = redux_max(m);
+            m = redux_max(largest(v));
         }
         const float m0 = m == NEG_INF ? 0.0f : m;
         if (by_z) {
@@ -276,30 +324,31 @@ __global__ void __launch_bounds__(VPL <= 32 ? 256 : 128, gate_ctas(VPL))
             for (int j = 0; j < VPL; ++j) nan |= v[j] != v[j];
             nan |= !sigmoid && m == __int_as_float(0x7f800000);
             if (!sigmoid && !o.renorm) {
-                float part = 0.0f;
+                float part[4] = {};
 #pragma unroll
-                for (int j = 0; j < VPL; ++j) part += __expf(v[j] - m0);
-                S = warp_sum(part);
+                for (int j = 0; j < VPL; ++j) part[j % 4] += __expf(v[j] - m0);
+                S = warp_sum((part[0] + part[1]) + (part[2] + part[3]));
                 inv_S = S > 0.0f ? __fdividef(1.0f, S) : 0.0f;
             }
         } else {
-            float part = 0.0f;  // NaN where a logit is
+            float part[4] = {};  // NaN where a logit is
             if (sigmoid) {
 #pragma unroll
                 for (int j = 0; j < VPL; ++j) {
                     v[j] = __fdividef(1.0f, 1.0f + __expf(-v[j]));
-                    part += v[j];
+                    part[0] += v[j];
                 }
             } else {
 #pragma unroll
                 for (int j = 0; j < VPL; ++j) {
                     v[j] = __expf(v[j] - m0);
-                    part += v[j];
+                    part[j % 4] += v[j];
                 }
-                S = warp_sum(part);
+                S = warp_sum((part[0] + part[1]) + (part[2] + part[3]));
                 inv_S = S > 0.0f || S != S ? __fdividef(1.0f, S) : 0.0f;
             }
-            nan = bias_nan || part != part;
+            const float any = (part[0] + part[1]) + (part[2] + part[3]);
+            nan = bias_nan || any != any;
             // a place past E has score 0 and key -inf
             if (bias) {
 #pragma unroll
@@ -317,7 +366,7 @@ __global__ void __launch_bounds__(VPL <= 32 ? 256 : 128, gate_ctas(VPL))
                 if (sigmoid ? k < -700.0f : m0 - k > 700.0f) return __int_as_float(0x7f800000);
                 return 1e-13f + (sigmoid ? 1e-15f * __expf(fminf(k, 80.0f)) : 0.0f);
             }
-            const float rel = (sigmoid ? 0x1p-16f : 0x1p-15f) * (k - bmin), all = (sigmoid ? 7.0f : 56.0f * inv_S) * U23;
+            const float rel = (sigmoid ? 0x1p-16f : 0x1p-15f) * (k - bmin), all = (sigmoid ? 7.0f : 33.0f * inv_S) * U23;
             return fminf(rel, all) + U23 * fabsf(k) + 1e-37f;
         };
         // kept: the groups that stay (0: a key or a group's score is NaN)
@@ -372,19 +421,22 @@ __global__ void __launch_bounds__(VPL <= 32 ? 256 : 128, gate_ctas(VPL))
         int total = 0;
         if (kept) {
             // the K-th largest of the lanes' largest keys is at most the K-th largest key
-            float top = NEG_INF;
-#pragma unroll
-            for (int j = 0; j < VPL; ++j) top = fmaxf(top, v[j]);
-            const float tau = __shfl_sync(FULL, sort_descending(top), K - 1);
+            const float tau = __shfl_sync(FULL, sort_descending(largest(v), dir), K - 1);
             const float least = tau - 2.0f * error_of(tau) - U23 * fabsf(tau);
             if (least > NEG_INF) {
-                // bits of the places that hold candidates: low and high half of VPL
-                uint32_t bits[(VPL + 31) / 32] = {};
-#pragma unroll
-                for (int j = 0; j < VPL; ++j) bits[j / 32] |= v[j] >= least ? 1u << (j % 32) : 0u;
+                // the places that hold candidates, as bits of numbers below 2^16
+                constexpr int WORDS = (VPL + 15) / 16;
+                uint32_t bits[WORDS];
                 int mine = 0;
 #pragma unroll
-                for (int h = 0; h < (VPL + 31) / 32; ++h) mine += __popc(bits[h]);
+                for (int h = 0; h < WORDS; ++h) {
+                    float sum = 0.0f;
+#pragma unroll
+                    for (int j = (16 * h + 15 < VPL ? 16 * h + 15 : VPL - 1); j >= 16 * h; --j)
+                        sum = fmaf(sum, 2.0f, is_ge(v[j], least));
+                    bits[h] = static_cast<uint32_t>(sum);
+                    mine += __popc(bits[h]);
+                }
                 int before = mine;
 #pragma unroll
                 for (int w = 1; w < 32; w <<= 1) {
@@ -396,9 +448,9 @@ __global__ void __launch_bounds__(VPL <= 32 ? 256 : 128, gate_ctas(VPL))
                 if (total <= 32) {
                     before -= mine;
 #pragma unroll
-                    for (int h = 0; h < (VPL + 31) / 32; ++h)
+                    for (int h = 0; h < WORDS; ++h)
                         while (bits[h]) {
-                            cand[before++] = lane + 32 * (32 * h + __ffs(bits[h]) - 1);
+                            cand[before++] = lane + 32 * (16 * h + __ffs(bits[h]) - 1);
                             bits[h] &= bits[h] - 1;
                         }
                 }
@@ -420,19 +472,28 @@ __global__ void __launch_bounds__(VPL <= 32 ? 256 : 128, gate_ctas(VPL))
                 } else if (sigmoid) {
                     const float s = __fdividef(1.0f, 1.0f + __expf(-z));
                     k = s + b;
-                    err = s * (6.0f + 1.2f * fminf(fmaxf(-z, 0.0f), 88.0f)) * U23 + U23 * fabsf(k) + 1e-37f;
+                    err = s * (3.5f + (1.0f - s) * (2.0f + 1.2f * fminf(fabsf(z), 88.0f))) * U23 + U23 * fabsf(k) + 1e-37f;
                 } else {
                     const float s = __expf(z - m0) * inv_S;
                     k = s + b;
-                    err = s * (56.0f + 1.7f * fminf(m0 - z, 88.0f)) * U23 + U23 * fabsf(k) + 1e-37f;
+                    err = s * (33.0f + 1.7f * fminf(m0 - z, 88.0f)) * U23 + U23 * fabsf(k) + 1e-37f;
                 }
             }
-            int rank = 0;
+            float above = 0.0f, level = 0.0f;  // candidates with a larger key, and with a key as large or larger
 #pragma unroll 4
             for (int q = 0; q < total; ++q) {
                 const float kq = __shfl_sync(FULL, k, q);
-                const int iq = __shfl_sync(FULL, i, q);
-                rank += kq > k || (kq == k && iq < i);
+                above += is_gt(kq, k);
+                level += is_ge(kq, k);
+            }
+            int rank = static_cast<int>(above);
+            if (__any_sync(FULL, lane < total && level - above > 1.0f)) {  // equal keys: lower expert first
+                rank = 0;
+                for (int q = 0; q < total; ++q) {
+                    const float kq = __shfl_sync(FULL, k, q);
+                    const int iq = __shfl_sync(FULL, i, q);
+                    rank += kq > k || (kq == k && iq < i);
+                }
             }
             // neighbours in the order: apart by their bounds, or equal in logit and bias
             __syncwarp();
