@@ -149,17 +149,10 @@ __device__ __forceinline__ float is_gt(float a, float b) {
 // 64-bit softmax denominator of a row with maximum m (1 for a row of -inf, whose scores are 0).
 template <class LT>
 __device__ __noinline__ double softmax_sum64(const LT* zt, int E, float m) {
-    // four exponentials at a time: one alone is a long chain of dependent operations
-    double part[4] = {};
+    double part = 0.0;
     const bool none = m < 0.0f && isinf(m);
-    for (int base = threadIdx.x & 31; base < E && !none; base += 128) {
-        float z[4];
-#pragma unroll
-        for (int q = 0; q < 4; ++q) z[q] = base + 32 * q < E ? load_logit(zt + base + 32 * q) : __int_as_float(0xff800000);
-#pragma unroll
-        for (int q = 0; q < 4; ++q) part[q] += exp(static_cast<double>(z[q]) - m);
-    }
-    const double S = warp_sum((part[0] + part[1]) + (part[2] + part[3]));
+    for (int i = threadIdx.x & 31; i < E && !none; i += 32) part += exp(static_cast<double>(load_logit(zt + i)) - m);
+    const double S = warp_sum(part);
     return S == 0.0 ? 1.0 : S;
 }
 
