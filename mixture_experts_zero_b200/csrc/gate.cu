@@ -21,8 +21,11 @@
 // K-th largest, sorts them, and evaluates them again in 64 bits where two neighbours in that order
 // are not apart by their bounds (a few tokens in a thousand).
 //
-// One warp per token, E / 32 logits a lane. What bounds it is instructions: per logit a load, an
-// exponential, a key and three comparisons, then about 300 a token for the choice.
+// One warp per token, E / 32 logits a lane, each read once. What bounds it is instructions and their
+// latency: per logit a load, an exponential, a key and three comparisons, then some hundreds a token
+// for the choice (about 1050 in all at E = 768). Measured on a B200 with inputs that are not in L2:
+// 16384 x 768 softmax with a bias, K = 12, in 37 us (1.4 TB/s); with 8 groups of sigmoid scores 51 us; one
+// token in 5 us. The choice by K rounds over all keys in 64 bits took 457 and 412 us.
 #include <cuda_bf16.h>
 
 #include "common.cuh"
