@@ -595,6 +595,8 @@ def _empty(stream, device, dtype, shape):
 @functools.lru_cache(maxsize=1024)
 def _shape_arg(T, d, N, Z, K, I):
     """A shape argument (read only), made once for each shape."""
+    if max(T, d, N, Z, K, I) >= 2 ** 31:  # the struct's fields are 32 bits wide
+        raise LcMoeError(ERR_UNSUPPORTED_SHAPE, "shape")
     return ctypes.byref(Shape(T, d, N, Z, K, I))
 
 

@@ -20,7 +20,8 @@ CASES = [
     # T, E, K, groups, top, rank
     (1, 1, 1, 1, 1, 1), (1, 768, 12, 1, 1, 1), (37, 12, 3, 4, 2, 2), (64, 33, 7, 1, 1, 1), (5, 2048, 32, 1, 1, 1),
     (9, 2048, 32, 32, 7, 2), (130, 768, 12, 8, 4, 2), (33, 96, 6, 3, 1, 1), (20, 333, 7, 9, 5, 2), (17, 64, 32, 32, 16, 2),
-    (11, 31, 31, 31, 31, 2), (21, 1025, 9, 1, 1, 1), (13, 40, 8, 8, 8, 1), (700, 130, 5, 2, 1, 2),
+    (11, 31, 31, 31, 31, 2), (21, 1025, 9, 1, 1, 1), (13, 40, 8, 8, 8, 1), (700, 130, 5, 2, 1, 2), (15, 32, 16, 32, 16, 2), (9, 30, 10, 3, 1, 2),
+    (8, 62, 2, 31, 1, 1),
 ]
 
 
@@ -289,3 +290,47 @@ def test_gate_on_another_stream_and_in_a_graph(cuda_device):
         g.replay()
         torch.cuda.synchronize()
         assert torch.equal(idx, want[0]) and torch.equal(gate, want[1]) and torch.equal(d, want_d)
+
+
+def test_binding_refuses_wrong_tensors(cuda_device):
+    z = logits_of(6, 16, 0, False)
+    b = torch.zeros(16, device="cuda")
+    with pytest.raises(ValueError, match="contiguous"):
+        B.lc_moe_gate(z.t().contiguous().t(), b, 2, 16)
+    with pytest.raises(TypeError, match="bias"):
+        B.lc_moe_gate(z, b.double(), 2, 16)
+    with pytest.raises(ValueError, match="bias"):
+        B.lc_moe_gate(z, b[:8], 2, 16)
+    with pytest.raises(ValueError, match="ws"):
+        B.lc_moe_gate(z, b, 2, 16, ws=torch.zeros(256, dtype=torch.uint8))
+    with pytest.raises(B.LcMoeError, match="unsupported shape"):
+        B.lc_moe_gate(z, b, 17, 16)
+    with pytest.raises(B.LcMoeError, match="workspace"):
+        B.lc_moe_gate(z, b, 2, 16, ws=torch.zeros(64, dtype=torch.uint8, device="cuda"))
+    idx, gate = B.lc_moe_gate(z, b, 2, 16)
+    with pytest.raises(B.LcMoeError, match="invalid argument"):
+        B.lc_moe_gate_backward(z, idx, gate, dlogits=z)
+    with pytest.raises(TypeError, match="dlogits"):
+        B.lc_moe_gate_backward(z, idx, gate, dlogits=z.bfloat16())
+    x = torch.zeros(6, 64, dtype=torch.bfloat16, device="cuda")
+    with pytest.raises(B.LcMoeError, match="invalid argument"):
+        B.lc_moe_combine_backward(x, x.clone(), x.clone(), gate, idx, dx=x)
+    with pytest.raises(B.LcMoeError):
+        B._shape_arg(2 ** 32 + 5, 64, 1, 0, 1, 64)
+
+
+def test_calls_on_two_streams_at_once(cuda_device):
+    """Two streams, one status word: nothing else is shared between calls."""
+    z = [logits_of(3000, 96, s, False) for s in (1, 2)]
+    ws = torch.zeros(256, dtype=torch.uint8, device="cuda")
+    want = [B.lc_moe_gate(v, None, 6, 64, score="sigmoid", groups=8, top_groups=4, group_rank=2) for v in z]
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream(), torch.cuda.Stream()]
+    got = []
+    for _ in range(5):
+        got.append([B.lc_moe_gate(v, None, 6, 64, score="sigmoid", groups=8, top_groups=4, group_rank=2, ws=ws, stream=s)
+                    for v, s in zip(z, streams)])
+    torch.cuda.synchronize()
+    for pair in got:
+        for a, b in zip(pair, want):
+            assert torch.equal(a[0], b[0]) and torch.equal(a[1], b[1])

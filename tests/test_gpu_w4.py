@@ -153,6 +153,52 @@ def test_ffn_large_activations(cuda_device):
     check_ffn(x, [4, 2], q, group, d, I, h, y)
 
 
+def test_a_row_of_nan_or_infinity_stays_by_itself(cuda_device):
+    N, d, I, group, counts = 3, 192, 128, 64, [5, 11, 20]
+    _, _, q = weights(N, d, I, group, 14)
+    rows = sum(counts)
+    x = torch.randn(rows, d, device="cuda").bfloat16()
+    off = torch.tensor([0, 5, 16, 36], dtype=torch.int32, device="cuda")
+    h, y = B.lc_moe_expert_ffn_w4(x, off, *q, rows, 1)
+    bad = x.clone()
+    for r, v in ((4, float("nan")), (7, float("inf")), (15, float("nan")), (30, float("-inf"))):
+        bad[r, 3] = v
+    h2, y2 = B.lc_moe_expert_ffn_w4(bad, off, *q, rows, 1)
+    keep = [r for r in range(rows) if r not in (4, 7, 15, 30)]
+    assert torch.equal(h[keep], h2[keep]) and torch.equal(y[keep], y2[keep])
+    for r in (4, 7, 15, 30):
+        assert not torch.isfinite(y2[r].float()).any()
+
+
+def test_rows_before_the_first_expert_stay(cuda_device):
+    N, d, I, group = 2, 64, 64, 32
+    _, _, q = weights(N, d, I, group, 15)
+    x = torch.randn(12, d, device="cuda").bfloat16()
+    off = torch.tensor([3, 3, 10], dtype=torch.int32, device="cuda")
+    h = torch.full((12, I), SENTINEL, dtype=torch.int16, device="cuda").view(torch.bfloat16)
+    y = torch.full((12, d), SENTINEL, dtype=torch.int16, device="cuda").view(torch.bfloat16)
+    B.lc_moe_expert_ffn_w4(x, off, *q, 12, 1, h=h, y=y)
+    for v in (h, y):
+        assert (v[:3].view(torch.int16) == SENTINEL).all() and (v[10:].view(torch.int16) == SENTINEL).all()
+    check_ffn(x, [0, 7], q, group, d, I, h, y, first=3)
+
+
+def test_ffn_on_two_streams_at_once(cuda_device):
+    N, d, I, group, counts = 4, 512, 256, 64, [2, 30, 0, 9]
+    _, _, q = weights(N, d, I, group, 16)
+    rows = sum(counts)
+    off = torch.tensor(np.concatenate([[0], np.cumsum(counts)]), dtype=torch.int32, device="cuda")
+    xs = [torch.randn(rows, d, device="cuda").bfloat16() for _ in range(2)]
+    want = [B.lc_moe_expert_ffn_w4(x, off, *q, rows, 1) for x in xs]
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream(), torch.cuda.Stream()]
+    got = [[B.lc_moe_expert_ffn_w4(x, off, *q, rows, 1, stream=s) for x, s in zip(xs, streams)] for _ in range(10)]
+    torch.cuda.synchronize()
+    for pair in got:
+        for a, b in zip(pair, want):
+            assert torch.equal(a[0], b[0]) and torch.equal(a[1], b[1])
+
+
 def test_bad_offsets_are_reported_and_skipped(cuda_device):
     N, d, I, group = 3, 64, 64, 32
     _, _, q = weights(N, d, I, group, 6)
