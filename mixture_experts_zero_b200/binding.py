@@ -555,7 +555,7 @@ def _one_device(**tensors):
 def _device_of(t, name):
     """The device of a call's first tensor: the current CUDA device, or an error."""
     d = t.device
-    if d.type != "cuda" or d.index != torch.cuda.current_device():
+    if not t.is_cuda or d.index != torch.cuda.current_device():
         _one_device(**{name: t})
     return d
 
@@ -586,10 +586,11 @@ def _on_stream(make, stream, *args, **kw):
         return make(*args, **kw)
 
 
-def _empty(stream, device, dtype, shape):
+def _empty2(stream, device, dtype, rows, cols):
+    """A new matrix (sizes as two arguments: a tuple costs torch.empty 0.7 us more)."""
     if stream is None:
-        return torch.empty(shape, dtype=dtype, device=device)
-    return _on_stream(torch.empty, stream, shape, dtype=dtype, device=device)
+        return torch.empty(rows, cols, dtype=dtype, device=device)
+    return _on_stream(torch.empty, stream, rows, cols, dtype=dtype, device=device)
 
 
 @functools.lru_cache(maxsize=1024)
@@ -636,9 +637,9 @@ def lc_moe_gate(logits, bias, K: int, N: int, score: str = "softmax", groups: in
     if gate is not None:
         _expect(gate, torch.float32, (T, K), dev, "gate")
     if idx is None:
-        idx = _empty(stream, dev, torch.int32, (T, K))
+        idx = _empty2(stream, dev, torch.int32, T, K)
     if gate is None:
-        gate = _empty(stream, dev, torch.float32, (T, K))
+        gate = _empty2(stream, dev, torch.float32, T, K)
     if ws is None:
         ws = _on_stream(_status_ws, stream, dev)
     _expect_ws(ws, dev)
@@ -665,7 +666,7 @@ def lc_moe_gate_backward(logits, idx, dgate, score: str = "softmax", renorm: boo
     if dlogits is not None:
         _expect(dlogits, logits.dtype, (T, E), dev, "dlogits")
     if dlogits is None:
-        dlogits = _empty(stream, dev, logits.dtype, (T, E))
+        dlogits = _empty2(stream, dev, logits.dtype, T, E)
     if ws is None:
         ws = _on_stream(_status_ws, stream, dev)
     _expect_ws(ws, dev)
@@ -698,9 +699,9 @@ def lc_moe_combine_backward(dout, x, y, gate, pair_row, dy=None, dgate=None, dx=
     if dy is None:
         dy = _on_stream(torch.zeros, stream, rows, d, dtype=torch.bfloat16, device=dev)
     if dgate is None:
-        dgate = _empty(stream, dev, torch.float32, (T, K))
+        dgate = _empty2(stream, dev, torch.float32, T, K)
     if dx is None:
-        dx = _empty(stream, dev, torch.bfloat16, (T, d))
+        dx = _empty2(stream, dev, torch.bfloat16, T, d)
     if ws is None:
         ws = _on_stream(_status_ws, stream, dev)
     _expect_ws(ws, dev)
@@ -728,9 +729,9 @@ def lc_moe_quantize_w4(src, group: int = 64, codes=None, scale=None, stream=None
     if scale is not None:
         _expect(scale, torch.bfloat16, (*lead, rows // 16, cols // group, 16), dev, "scale")
     if codes is None:
-        codes = _empty(stream, dev, torch.uint8, (*lead, rows, cols // 2))
+        codes = _on_stream(torch.empty, stream, (*lead, rows, cols // 2), dtype=torch.uint8, device=dev)
     if scale is None:
-        scale = _empty(stream, dev, torch.bfloat16, (*lead, rows // 16, cols // group, 16))
+        scale = _on_stream(torch.empty, stream, (*lead, rows // 16, cols // group, 16), dtype=torch.bfloat16, device=dev)
     if src.numel():
         _check(_lib().lc_moe_quantize_w4(src.data_ptr(), src.numel() // cols, cols, group, codes.data_ptr(),
                                          scale.data_ptr(), _raw_stream(stream, dev)), "lc_moe_quantize_w4")
@@ -768,9 +769,9 @@ def lc_moe_expert_ffn_w4(x_perm, offsets, w13q, w13_scale, w2q, w2_scale, T: int
     if y is not None:
         _expect(y, torch.bfloat16, (rows, d), dev, "y")
     if h is None:
-        h = _empty(stream, dev, torch.bfloat16, (rows, I))
+        h = _empty2(stream, dev, torch.bfloat16, rows, I)
     if y is None:
-        y = _empty(stream, dev, torch.bfloat16, (rows, d))
+        y = _empty2(stream, dev, torch.bfloat16, rows, d)
     if ws is None:
         ws = _on_stream(_status_ws, stream, dev)
     _expect_ws(ws, dev)
@@ -810,7 +811,7 @@ def lc_moe_forward_w4(x, wr, bias, w13q, w13_scale, w2q, w2_scale, K: int, opts:
         _expect(counts, torch.int32, (E,), dev, "counts")
     s = _shape_arg(T, d, N, E - N, K, I)
     if out is None:
-        out = _empty(stream, dev, torch.bfloat16, (T, d))
+        out = _empty2(stream, dev, torch.bfloat16, T, d)
     if ws is None:
         ws = _on_stream(new_workspace, stream, Shape(T, d, N, E - N, K, I), OP_FORWARD_W4, dev)
     _expect_ws(ws, dev)
