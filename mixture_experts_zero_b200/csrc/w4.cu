@@ -338,9 +338,8 @@ __global__ void __launch_bounds__(W4_THREADS, W4_CTAS) w4_kernel(const W4Args a)
     const uint32_t sc_step = 2048u / static_cast<uint32_t>(a.group);  // scale bytes per 64 columns
     Cursor pc = begin();
     int p_ks = nk;
-    uint32_t p_slot = 0;
     const uint8_t *p_codes = nullptr, *p_scale = nullptr;
-    auto produce = [&](auto half) {
+    auto produce = [&](auto half, uint32_t slot) {  // slot: byte offset in the ring
         constexpr int H = decltype(half)::value;
         if (H == 0) {
             while (p_ks >= nk && pc.rt < row_tiles) {  // next item in which this warp's team has a tile
@@ -356,7 +355,7 @@ __global__ void __launch_bounds__(W4_THREADS, W4_CTAS) w4_kernel(const W4Args a)
             }
         }
         if (p_ks < nk) {
-            const uint32_t dst = ring + p_slot;
+            const uint32_t dst = ring + slot;
             const uint8_t* c = H ? p_codes + (SWIGLU ? 2 : 4) * a.code_blk : p_codes;
             const uint8_t* up = c + a.code_up;
             cp_async16(dst, c);
@@ -364,20 +363,19 @@ __global__ void __launch_bounds__(W4_THREADS, W4_CTAS) w4_kernel(const W4Args a)
             cp_async16(dst + 1024, up);
             cp_async16(dst + 1536, up + a.code_blk);
             const uint8_t* sc = (H ? p_scale + (SWIGLU ? 2 : 4) * a.scale_blk : p_scale) + (p_ks * sc_step & ~31u);
-            cp_async4(ring_sc + p_slot, sc);
-            if (G32) cp_async4(ring_sc + p_slot + 128, sc + 32);
+            cp_async4(ring_sc + slot, sc);
+            if (G32) cp_async4(ring_sc + slot + 128, sc + 32);
             if (H == HALVES - 1) {
                 p_codes += a.split * 512;
                 p_ks += a.split;
             }
-            p_slot = p_slot == (STAGES - 1) * STAGE_BYTES ? 0u : p_slot + STAGE_BYTES;
         }
         cp_async_commit();
     };
     static_assert(STAGES == 4 && HALVES <= 2, "the halves alternate through the ring's prologue");
-    produce(Int<0>());
-    produce(Int<HALVES - 1>());
-    produce(Int<0>());
+    produce(Int<0>(), 0);
+    produce(Int<HALVES - 1>(), STAGE_BYTES);
+    produce(Int<0>(), 2 * STAGE_BYTES);
 
     // the gate/up product lets the down product start; the down product waits for it before it reads
     // H (weights and offsets are older than both kernels)
@@ -421,8 +419,11 @@ __global__ void __launch_bounds__(W4_THREADS, W4_CTAS) w4_kernel(const W4Args a)
         xn = rows_of(nx);
         load_x(xa, xn, nx.rows);
     }
-    uint32_t slot = 0;
-    int buf = 0;
+    // Steps take turns on xa and xb; which is next carries over from item to item, and with two halves
+    // a step so do the ring's slots, which are then constants (0 and 1 go with xa). With one half they
+    // are counted: the next one to read and the one before it, which the producer fills.
+    int turn = 0, buf = 0;
+    uint32_t slot = 0, last = (STAGES - 1) * STAGE_BYTES;
     const uint8_t* my_ring = s_raw + warp * STAGES * STAGE_BYTES;
     const int steps = (nk - kw + a.split - 1) / a.split;
     const int x_step = a.split * 64;
@@ -446,40 +447,44 @@ __global__ void __launch_bounds__(W4_THREADS, W4_CTAS) w4_kernel(const W4Args a)
         if (mine) {
             int left = steps;
             // one step on the activations `v`, while those of the next step (of this item or the next) load into `w`
-            auto step = [&](auto nt, uint4 (&v)[MAXNT][2], uint4 (&w)[MAXNT][2]) {
+            auto step = [&](auto nt, auto odd, uint4 (&v)[MAXNT][2], uint4 (&w)[MAXNT][2]) {
                 constexpr int NT = decltype(nt)::value;
                 xr.p += x_step;
                 if (--left) load_x(w, xr, it.rows);
                 else if (more) load_x(w, xn, nx.rows);
                 auto half = [&](auto h, auto ahead) {
+                    constexpr int H = decltype(h)::value, S = 2 * decltype(odd)::value + H;
                     cp_async_wait<STAGES - 2>();
                     __syncwarp();  // the stage is visible, and the slot before it has been read by every lane
-                    produce(ahead);
-                    w4_stage<NT, MAXNT, G32>(my_ring + slot, lane, v, acc + 4 * decltype(h)::value);
-                    slot = slot == (STAGES - 1) * STAGE_BYTES ? 0u : slot + STAGE_BYTES;
+                    if (HALVES > 1) {
+                        produce(ahead, (S + STAGES - 1) % STAGES * STAGE_BYTES);
+                        w4_stage<NT, MAXNT, G32>(my_ring + S * STAGE_BYTES, lane, v, acc + 4 * H);
+                    } else {
+                        produce(ahead, last);
+                        w4_stage<NT, MAXNT, G32>(my_ring + slot, lane, v, acc);
+                        last = slot;
+                        slot = slot == (STAGES - 1) * STAGE_BYTES ? 0u : slot + STAGE_BYTES;
+                    }
                 };
                 half(Int<0>(), Int<HALVES - 1>());
                 if (HALVES > 1) half(Int<HALVES - 1>(), Int<0>());
             };
             auto run = [&](auto nt) {
-                while (true) {
-                    step(nt, xa, xb);
-                    if (!left) {
-#pragma unroll
-                        for (int n = 0; n < MAXNT; ++n) {
-                            xa[n][0] = xb[n][0];
-                            xa[n][1] = xb[n][1];
-                        }
-                        break;
+                while (left) {
+                    if (turn == 0) {
+                        step(nt, Int<0>(), xa, xb);
+                        turn = 1;
+                        if (!left) break;
                     }
-                    step(nt, xb, xa);
-                    if (!left) break;
+                    step(nt, Int<1>(), xb, xa);
+                    turn = 0;
                 }
             };
             if (MAXNT > 1 && it.rows > 8) run(Int<MAXNT>());
             else run(Int<1>());
         } else if (more) {
-            load_x(xa, xn, nx.rows);
+            if (turn == 0) load_x(xa, xn, nx.rows);
+            else load_x(xb, xn, nx.rows);
         }
         // join the team's partial sums, 8 rows x 64 weight rows at a time (two buffers: one barrier each)
 #pragma unroll
