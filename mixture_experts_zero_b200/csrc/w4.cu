@@ -27,12 +27,13 @@
 // weight.
 //
 // Measured on a B200 (copy rate 6.5 TB/s): 32 tokens over 115 experts of 6144 x 2048, group 64, 2.3 GB
-// in 461 us (5.0 TB/s); 128 tokens over 512 experts, 9.0 GB in 1.97 ms; one token over 8 experts, 156 MB
-// in 48 us. It is bound by instructions: 7 integer operations for 8 weights on a half-rate pipe, and
+// in 455 us (5.1 TB/s); 128 tokens over 512 experts, 9.0 GB in 1.95 ms; one token over 8 experts, 156 MB
+// in 47 us. It is bound by instructions: 7 integer operations for 8 weights on a half-rate pipe, and
 // the mma.sync next to them (the stream without the products takes 345 us, without unpacking 374).
 // No gain came from byte permutes or multiplications in place of shifts, from more logic operations
-// for fewer shifts, from products of 16 + n that start at -24 times the sum of the activations, from
-// ring stages of one block by 256 columns, or from 24 warps an SM. With many rows an expert it
+// for fewer shifts, from products of 16 + n or 128 + n that start at -24 or -136 times the sum of the
+// activations (which drops the subtraction), from ring stages of one block by 256 columns, or from
+// 24 warps an SM. With many rows an expert it
 // reaches 0.13 to 0.21 PFLOP/s.
 #include "common.cuh"
 
