@@ -501,7 +501,11 @@ __global__ void __launch_bounds__(VPL <= 32 ? 256 : 128, gate_ctas(VPL))
             const float z_s = __shfl_sync(FULL, z, from), b_s = __shfl_sync(FULL, b, from);
             const float k_n = __shfl_down_sync(FULL, k_s, 1), e_n = __shfl_down_sync(FULL, e_s, 1);
             const float z_n = __shfl_down_sync(FULL, z_s, 1), b_n = __shfl_down_sync(FULL, b_s, 1);
-            const bool close = lane < K && lane + 1 < total && !(k_s - k_n > e_s + e_n) && !(z_s == z_n && b_s == b_n);
+            // Equal keys at the K-th place may have others behind them that fp32 cannot tell from them: the
+            // pairs that count reach to the end of that run.
+            const bool same = z_s == z_n && b_s == b_n;
+            const int last = K - 2 + __ffs(~(__ballot_sync(FULL, same) >> (K - 1)));
+            const bool close = lane <= last && lane + 1 < total && !(k_s - k_n > e_s + e_n) && !same;
             my_idx = i_s;
             z = z_s;
             if (__any_sync(FULL, close)) {

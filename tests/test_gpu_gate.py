@@ -138,6 +138,27 @@ def test_masked_logits_and_switched_off_experts(cuda_device, score):
     check_gate(z, b, K, 24, score, groups=8, top=3, rank=2)
 
 
+@pytest.mark.parametrize("score", ["softmax", "sigmoid"])
+def test_scores_below_fp32_behind_masked_experts(cuda_device, score):
+    """Masked experts (score 0) tie in fp32 with scores that only 64 bits can hold: a run of equal keys
+    across the K-th place hides an expert behind it that belongs before it."""
+    E, K = 22, 5
+    low = -300.0 if score == "softmax" else -120.0
+    z = torch.full((6, E), -math.inf, device="cuda")
+    z[:, 4] = 1.0
+    z[0, 15] = low
+    z[1, 15], z[1, 20] = low, low + 1
+    z[2, 0] = low
+    z[3, 5:] = low
+    z[4, 21] = low
+    z[5, 6], z[5, 21] = low, low
+    for b in (None, torch.zeros(E, device="cuda")):
+        check_gate(z, b, K, E, score)
+        check_gate(z, b, K, E, score, renorm=False)
+        check_gate(z, b, K, E, score, groups=2, top=1, rank=2)
+        check_gate(z.repeat(1, 3), None if b is None else b.repeat(3), K, E, score, groups=3, top=2, rank=2)
+
+
 def test_all_masked_row_has_zero_gates(cuda_device):
     z = torch.full((2, 16), -math.inf, device="cuda")
     for score in ("softmax", "sigmoid"):
