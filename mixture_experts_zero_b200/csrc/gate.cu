@@ -77,15 +77,21 @@ __device__ __forceinline__ int arg_max(unsigned long long k, int i) {
 }
 
 __device__ __forceinline__ double sigmoid64(double z) { return 1.0 / (1.0 + exp(-z)); }
-__device__ __forceinline__ float sigmoid32(float z) { return 1.0f / (1.0f + expf(-z)); }
+// from e^-|z|, which does not overflow
+__device__ __forceinline__ float sigmoid32(float z) {
+    const float e = expf(-fabsf(z));
+    return (z < 0.0f ? e : 1.0f) / (1.0f + e);
+}
 
-// p_r of the chosen logits (lane r < K; other lanes pass z = -inf and get 0): s_r / sum of the
-// chosen s. Where the largest chosen logit of a sigmoid is below -40, 1 + e^z is 1 in fp32 and the
-// quotient is the softmax of the chosen logits, which cannot underflow. All -inf: 0.
+// p_r of the chosen logits (lane r < K; other lanes pass z = -inf and get 0): s_r / sum of the chosen
+// s. Sigmoids of negative logits are e^z / (1 + e^z), all of them times the same e^-m where the largest
+// chosen logit m is negative, so that no quotient underflows before its share does. All -inf: 0.
 __device__ __forceinline__ float chosen_share(float z, bool sigmoid) {
     const float m = warp_max(z);
     if (m == __int_as_float(0xff800000)) return z != z ? z : 0.0f;
-    const float s = (sigmoid && !(m < -40.0f)) ? sigmoid32(z) : expf(z - m);
+    float s;
+    if (!sigmoid) s = expf(z - m);
+    else s = z < 0.0f ? expf(z - fminf(m, 0.0f)) / (1.0f + expf(z)) : sigmoid32(z);
     return s / warp_sum(s);
 }
 

@@ -159,6 +159,15 @@ def test_scores_below_fp32_behind_masked_experts(cuda_device, score):
         check_gate(z.repeat(1, 3), None if b is None else b.repeat(3), K, E, score, groups=3, top=2, rank=2)
 
 
+def test_small_shares_of_sigmoid_gates(cuda_device):
+    """A chosen score whose e^-z does not fit fp32 still has its share of the gates."""
+    z = torch.tensor([[-30.0, -90.0, -95.0, -200.0], [3.0, -70.0, -88.0, -100.0], [-39.0, -89.5, -101.0, -110.0]],
+                     device="cuda")
+    for scale in (1.0, 2.5):
+        check_gate(z, None, 3, 4, "sigmoid", scale=scale)
+        check_gate(z, torch.zeros(4, device="cuda"), 3, 4, "sigmoid", scale=scale)
+
+
 def test_all_masked_row_has_zero_gates(cuda_device):
     z = torch.full((2, 16), -math.inf, device="cuda")
     for score in ("softmax", "sigmoid"):
