@@ -654,9 +654,12 @@ __global__ void __launch_bounds__(GATE_THREADS)
         D = warp_sum(mine);
     } else if (o.renorm) {
         const float p = chosen_share(z, sigmoid);
-        const float mean = warp_sum(p * dg);
         const float f = sigmoid ? 1.0f / (1.0f + expf(z)) : 1.0f;
-        mine = p * f * (dg - mean);
+        // dg_r - sum_q p_q dg_q as sum_q p_q (dg_r - dg_q): a pick that has nearly all of the share does
+        // not lose its small gradient in the difference
+        float apart = 0.0f;
+        for (int q = 0; q < K; ++q) apart = fmaf(__shfl_sync(FULL, p, q), dg - __shfl_sync(FULL, dg, q), apart);
+        mine = p * f * apart;
     } else {
         const float q = expf(-fabsf(z));
         mine = dg * q / ((1.0f + q) * (1.0f + q));

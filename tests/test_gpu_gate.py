@@ -284,6 +284,28 @@ def test_gate_gradient_against_differences(cuda_device, renorm, score):
         assert np.abs(got[:, e] - diff).max() <= 2e-6 * np.abs(w).sum(1).max() + 1e-6
 
 
+@pytest.mark.parametrize("score", ["softmax", "sigmoid"])
+def test_gradient_of_a_pick_with_nearly_all_of_the_share(cuda_device, score):
+    """The largest pick's gradient is a sum over the others, not the difference of two numbers that are
+    nearly equal: relative to itself it is within (2 R + 64) half steps, one half step more for each of
+    K differences."""
+    z = torch.tensor([[9.0, -9.0, -12.0, -30.0], [40.0, 3.0, 2.0, 1.0]], device="cuda")
+    idx = torch.tensor([[0, 1, 2], [0, 1, 2]], dtype=torch.int32, device="cuda")
+    dg = torch.tensor([[0.7, -1.3, 2.1], [1.0, 0.9, -4.0]], device="cuda")
+    got = f64(B.lc_moe_gate_backward(z, idx, dg, score=score))
+    s = R.scores(f64(z), score)[:, :3]
+    if score == "sigmoid":  # 1 - s without its rounding
+        f = 1.0 / (1.0 + np.exp(f64(z)[:, :3]))
+    else:
+        f = np.ones((2, 3))
+    p = s / s.sum(1, keepdims=True)
+    d = f64(dg)
+    want = p * f * (p[:, None, :] * (d[:, :, None] - d[:, None, :])).sum(2)
+    size = p * f * (p[:, None, :] * np.abs(d[:, :, None] - d[:, None, :])).sum(2)
+    assert np.all(np.abs(got[:, :3] - want) <= (2 * 39 + 64 + 3) * R.U32 * size)
+    assert np.all(got[:, 3] == 0)
+
+
 def test_gate_gradient_repeated_and_bad_picks(cuda_device):
     z = logits_of(4, 30, 3, False)
     idx = torch.tensor([[1, 1, 5, 1], [0, 29, 0, 29], [2, -1, 30, 4], [7, 8, 9, 10]], dtype=torch.int32, device="cuda")
