@@ -9,6 +9,8 @@ from __future__ import annotations
 
 import ctypes
 import functools
+import math
+import operator
 import pathlib
 import threading
 
@@ -593,9 +595,14 @@ def _empty2(stream, device, dtype, rows, cols):
     return _on_stream(torch.empty, stream, rows, cols, dtype=dtype, device=device)
 
 
-@functools.lru_cache(maxsize=1024)
 def _shape_arg(T, d, N, Z, K, I):
-    """A shape argument (read only), made once for each shape."""
+    """A shape argument (read only), made once for each shape. T, d and I are sizes of tensors; what a
+    caller passes becomes a number before it is looked up."""
+    return _shape_of(T, d, operator.index(N), operator.index(Z), operator.index(K), I)
+
+
+@functools.lru_cache(maxsize=1024)
+def _shape_of(T, d, N, Z, K, I):
     if max(T, d, N, Z, K, I) >= 2 ** 31:  # the struct's fields are 32 bits wide
         raise LcMoeError(ERR_UNSUPPORTED_SHAPE, "shape")
     return ctypes.byref(Shape(T, d, N, Z, K, I))
@@ -607,12 +614,23 @@ def _dims_of(t, n, name):
     return tuple(t.shape)
 
 
-@functools.lru_cache(maxsize=1024)
 def _gate_opts(score, groups, top_groups, group_rank, renorm, scale):
-    """An options argument (read only), made once for each set of options."""
+    """An options argument (read only), made once for each set of options. They become plain numbers
+    before they are looked up: a tensor or an array is found by its identity, whatever it holds."""
+    if type(scale) is not float:
+        if isinstance(scale, (str, bytes, bytearray)):
+            raise TypeError(f"scale: expected a number, got {scale!r}")
+        scale = float(scale)
+    return _opts_of(score, operator.index(groups), operator.index(top_groups), operator.index(group_rank),
+                    bool(renorm), scale, math.copysign(1.0, scale))
+
+
+@functools.lru_cache(maxsize=1024)
+def _opts_of(score, groups, top_groups, group_rank, renorm, scale, sign):
+    # sign: 0.0 and -0.0 are equal but not the same factor
     if score not in SCORES:
         raise ValueError(f"score: expected one of {sorted(SCORES)}, got {score!r}")
-    return ctypes.byref(GateOpts(SCORES[score], groups, top_groups, group_rank, int(bool(renorm)), scale))
+    return ctypes.byref(GateOpts(SCORES[score], groups, top_groups, group_rank, int(renorm), scale))
 
 
 def lc_moe_gate(logits, bias, K: int, N: int, score: str = "softmax", groups: int = 1, top_groups: int = 1,

@@ -1,7 +1,9 @@
 """Host-side checks of the general gates, the gradients and the 4-bit experts: bad arguments are
 refused before any CUDA call, in the library and in the binding."""
 import ctypes
+import math
 
+import numpy as np
 import pytest
 import torch
 
@@ -167,3 +169,42 @@ class _Elsewhere:
 def test_binding_refuses_tensors_of_another_device():
     with pytest.raises(ValueError, match="current device"):
         B._one_device(x=_Elsewhere())
+
+
+def _options(*a):
+    return B._gate_opts(*a)._obj
+
+
+@pytest.mark.parametrize("make", [torch.tensor, np.array], ids=["tensor", "array"])
+def test_options_follow_a_scalar_that_changes(make):
+    """A factor held in a 0-d tensor or array is read anew by every call."""
+    scale = make(1.5)
+    assert _options("softmax", 1, 1, 1, True, scale).scale == 1.5
+    scale += 1.5
+    assert _options("softmax", 1, 1, 1, True, scale).scale == 3.0
+    groups, renorm = make(4), make(True)
+    first = _options("softmax", groups, groups, 1, renorm, 1.0)
+    assert (first.groups, first.top_groups, first.renorm) == (4, 4, 1)
+    groups *= 2
+    renorm &= False
+    second = _options("softmax", groups, groups, 1, renorm, 1.0)
+    assert (second.groups, second.top_groups, second.renorm) == (8, 8, 0)
+    assert (first.groups, first.renorm) == (4, 1)
+
+
+def test_shapes_follow_a_scalar_that_changes():
+    k = torch.tensor(3)
+    assert B._shape_arg(5, 64, 8, 4, k, 64)._obj.K == 3
+    k += 1
+    assert B._shape_arg(5, 64, 8, 4, k, 64)._obj.K == 4
+    assert B._shape_arg(5, 64, torch.tensor(8), torch.tensor(4), k, 64)._obj.N == 8
+
+
+def test_options_keep_the_sign_of_zero_and_refuse_what_is_no_number():
+    for scale in (0.0, -0.0, 0.0):
+        assert math.copysign(1.0, _options("softmax", 1, 1, 1, True, scale).scale) == math.copysign(1.0, scale)
+    for bad in ("1.5", None):
+        with pytest.raises(TypeError):
+            B._gate_opts("softmax", 1, 1, 1, True, bad)
+    with pytest.raises(TypeError):
+        B._gate_opts("softmax", 1.0, 1, 1, True, 1.0)
