@@ -630,6 +630,8 @@ def _opts_of(score, groups, top_groups, group_rank, renorm, scale, sign):
     # sign: 0.0 and -0.0 are equal but not the same factor
     if score not in SCORES:
         raise ValueError(f"score: expected one of {sorted(SCORES)}, got {score!r}")
+    if max(abs(groups), abs(top_groups), abs(group_rank)) >= 2 ** 31:  # the struct's fields are 32 bits wide
+        raise LcMoeError(ERR_INVALID_ARG, "options")
     return ctypes.byref(GateOpts(SCORES[score], groups, top_groups, group_rank, int(renorm), scale))
 
 

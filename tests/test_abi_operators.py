@@ -208,3 +208,13 @@ def test_options_keep_the_sign_of_zero_and_refuse_what_is_no_number():
             B._gate_opts("softmax", 1, 1, 1, True, bad)
     with pytest.raises(TypeError):
         B._gate_opts("softmax", 1.0, 1, 1, True, 1.0)
+
+
+@pytest.mark.parametrize("at", [0, 1, 2])
+def test_options_beyond_32_bits_are_refused(at):
+    """The struct's fields are 32 bits wide: 2^32 + 1 is not 1."""
+    for v in (2 ** 32 + 1, 2 ** 31, -2 ** 32 + 1):
+        a = [1, 1, 1]
+        a[at] = v
+        with pytest.raises(B.LcMoeError, match="invalid argument"):
+            B._gate_opts("softmax", *a, True, 1.0)
