@@ -240,12 +240,13 @@ __global__ void __launch_bounds__(W4_THREADS, W4_CTAS) w4_kernel(const W4Args a)
         int32_t* part = reinterpret_cast<int32_t*>(red);  // [2][W4_WARPS]
         const int per = (a.N + W4_THREADS - 1) / W4_THREADS, first = threadIdx.x * per;
         int rt[8], sum = 0, some = 0;
+        bool bad = false;
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
             rt[i] = 0;
             if (i < per && first + i < a.N) {
                 const int lo = __ldg(a.offsets + first + i), hi = __ldg(a.offsets + first + i + 1);
-                if (lo < 0 || hi < lo || hi > a.rows_cap) set_status(a.status, LC_MOE_DEV_IDX_RANGE);
+                if (lo < 0 || hi < lo || hi > a.rows_cap) bad = true;
                 else rt[i] = (hi - lo + TOK - 1) / TOK;
             }
             sum += rt[i];
@@ -264,26 +265,48 @@ __global__ void __launch_bounds__(W4_THREADS, W4_CTAS) w4_kernel(const W4Args a)
             part[warp] = sum_to;
             part[W4_WARPS + warp] = some_to;
         }
-        __syncthreads();
-        row_tiles = live = 0;
-#pragma unroll
-        for (int w = 0; w < W4_WARPS; ++w) {
-            if (w == warp) {
-                sum_to += row_tiles;
-                some_to += live;
+        if (__syncthreads_or(bad)) {
+            // Offsets that fall somewhere or leave [0, rows_cap]: experts may then share rows, and their tiles
+            // may add up to more than 32 bits hold. One thread takes the experts that are within bounds and
+            // begin where the last one taken ends, or behind it; these have rows of their own.
+            if (threadIdx.x == 0) {
+                set_status(a.status, LC_MOE_DEV_IDX_RANGE);
+                int end = 0, before = 0, taken = 0;
+                for (int e = 0; e < a.N; ++e) {
+                    const int lo = __ldg(a.offsets + e), hi = __ldg(a.offsets + e + 1);
+                    if (lo < end || hi <= lo || hi > a.rows_cap) continue;
+                    pre[taken] = before;
+                    ids[taken++] = static_cast<uint16_t>(e);
+                    before += (hi - lo + TOK - 1) / TOK;
+                    end = hi;
+                }
+                pre[taken] = before;
+                part[0] = taken;
             }
-            row_tiles += part[w];
-            live += part[W4_WARPS + w];
+            __syncthreads();
+            live = part[0];
+            row_tiles = pre[live];
+        } else {
+            row_tiles = live = 0;
+#pragma unroll
+            for (int w = 0; w < W4_WARPS; ++w) {
+                if (w == warp) {
+                    sum_to += row_tiles;
+                    some_to += live;
+                }
+                row_tiles += part[w];
+                live += part[W4_WARPS + w];
+            }
+            int at = some_to - some, before = sum_to - sum;
+#pragma unroll
+            for (int i = 0; i < 8; ++i)
+                if (rt[i] > 0) {
+                    pre[at] = before;
+                    ids[at++] = static_cast<uint16_t>(first + i);
+                    before += rt[i];
+                }
+            if (threadIdx.x == 0) pre[live] = row_tiles;
         }
-        int at = some_to - some, before = sum_to - sum;
-#pragma unroll
-        for (int i = 0; i < 8; ++i)
-            if (rt[i] > 0) {
-                pre[at] = before;
-                ids[at++] = static_cast<uint16_t>(first + i);
-                before += rt[i];
-            }
-        if (threadIdx.x == 0) pre[live] = row_tiles;
     }
     __syncthreads();
     const int tiles = a.m / (64 * HALVES), teams = W4_WARPS / a.split;

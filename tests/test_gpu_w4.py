@@ -211,6 +211,48 @@ def test_bad_offsets_are_reported_and_skipped(cuda_device):
         assert B.lc_moe_read_status(ws, raise_on_error=False) == B.DEV_IDX_RANGE
 
 
+@pytest.mark.parametrize("rows,offsets,taken", [
+    (8, [0, 3, 2, 8], [0]),            # expert 2 begins inside expert 0
+    (8, [0, 3, 6, 9], [0, 1]),
+    (8, [-1, 3, 6, 8], [1, 2]),
+    (8, [0, 100, 6, 8], [2]),
+    (40, [0, 9, 4, 12, 12, 40], [0, 4]),
+    (40, [20, 10, 15, 15, 41, 30, 40], [1, 5]),
+    (8, [8, 0, 0, -5, -9, 2 ** 31 - 1, 7], []),
+    (8, [0, -1, 0, 9, 8], []),
+])
+def test_experts_beside_bad_offsets(cuda_device, rows, offsets, taken):
+    """Only the rows of experts that are not skipped are written, with what good offsets give."""
+    N, d, I, group = len(offsets) - 1, 64, 64, 32
+    _, _, q = weights(N, d, I, group, 7)
+    x = torch.randn(rows, d, device="cuda").bfloat16()
+    ws = torch.zeros(256, dtype=torch.uint8, device="cuda")
+    h = torch.full((rows, I), SENTINEL, dtype=torch.int16, device="cuda").view(torch.bfloat16)
+    y = torch.full((rows, d), SENTINEL, dtype=torch.int16, device="cuda").view(torch.bfloat16)
+    B.lc_moe_expert_ffn_w4(x, torch.tensor(offsets, dtype=torch.int32, device="cuda"), *q, rows, 1, h=h, y=y, ws=ws)
+    assert B.lc_moe_read_status(ws, raise_on_error=False) == B.DEV_IDX_RANGE
+    rest = np.ones(rows, bool)
+    for e in taken:
+        a, b = offsets[e], offsets[e + 1]
+        check_ffn(x, [0] * e + [b - a], q, group, d, I, h, y, first=a)
+        rest[a:b] = False
+    for v in (h, y):
+        assert np.all(v.view(torch.int16).cpu().numpy()[rest] == SENTINEL)
+
+
+def test_offsets_that_give_many_experts_the_same_rows(cuda_device):
+    """1024 experts that all claim rows 0..64: the first has them, and no sum runs over."""
+    rows, N, d, I, group = 64, 2048, 64, 64, 32
+    _, _, q = weights(N, d, I, group, 8)
+    x = torch.randn(rows, d, device="cuda").bfloat16()
+    off = torch.zeros(N + 1, dtype=torch.int32, device="cuda")
+    off[1::2] = rows
+    ws = torch.zeros(256, dtype=torch.uint8, device="cuda")
+    h, y = B.lc_moe_expert_ffn_w4(x, off, *q, rows, 1, ws=ws)
+    assert B.lc_moe_read_status(ws, raise_on_error=False) == B.DEV_IDX_RANGE
+    check_ffn(x, [rows], q, group, d, I, h, y)
+
+
 def test_ffn_on_another_stream_in_a_graph_and_repeated(cuda_device):
     N, d, I, group, counts = 6, 256, 192, 64, [3, 0, 9, 20, 1, 2]
     _, _, q = weights(N, d, I, group, 12)
