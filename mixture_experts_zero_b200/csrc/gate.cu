@@ -395,6 +395,8 @@ __global__ void __launch_bounds__(VPL <= 32 ? 256 : 128, gate_ctas(VPL))
             }
             const bool two = o.group_rank == 2 && size > 1;
             float score = two ? a + b : a;
+            // two finite keys whose sum fp32 cannot hold: left to 64 bits, as a NaN
+            if (two && isinf(score) && !isinf(a) && !isinf(b)) score = __int_as_float(0x7fc00000);
             float err = two ? error_of(a) + error_of(b) + U23 * fabsf(score) : error_of(a);
             // lane g: group g
             score = __shfl_sync(FULL, score, (lane * team) & 31);
@@ -406,8 +408,8 @@ __global__ void __launch_bounds__(VPL <= 32 ? 256 : 128, gate_ctas(VPL))
                 rank += other > score || (other == score && q < lane);
             }
             kept = __ballot_sync(FULL, lane < o.groups && rank < o.top_groups);
-            // the groups that stay and those that leave are apart by their bounds (infinite scores have no
-            // bound and are what they are in 64 bits)
+            // the groups that stay and those that leave are apart by their bounds (a score with an infinite key
+            // has no bound and is what it is in 64 bits)
             const float low = redux_min(((kept >> lane) & 1u) ? score - err : __int_as_float(0x7f800000));
             const float high = redux_max(lane < o.groups && !((kept >> lane) & 1u) ? score + err : NEG_INF);
             if (!(low > high) || __any_sync(FULL, score != score)) {

@@ -235,6 +235,23 @@ def test_unaligned_rows_and_default_options(cuda_device):
         check_backward(v, idx, torch.ones_like(gate), "softmax", False, 1.0, d)
 
 
+@pytest.mark.parametrize("low", [torch.finfo(torch.float32).min, -3e38])
+@pytest.mark.parametrize("score", ["softmax", "sigmoid"])
+def test_lowest_value_biases_beside_infinite_ones(cuda_device, score, low):
+    """Two keys at the end of the fp32 range make a finite group score in 64 bits, above one of -inf; two
+    at the other end make one that is below +inf."""
+    inf = math.inf
+    z = logits_of(5, 8, 21, False)
+    for b in ([0, 0, -inf, -inf, low, low, -inf, -inf], [-inf, -inf, -inf, 0, low, low, low, low],
+              [low, low, -inf, -inf, 0, 0, low, 0], [-low, -low, 0, 0, -low, 0, -low, -low],
+              [low, -inf, low, low, low, 0, -inf, -inf]):
+        b = torch.tensor(b, device="cuda", dtype=torch.float32)
+        for top, K in ((1, 2), (2, 3), (3, 5)):
+            check_gate(z, b, K, 8, score, groups=4, top=top, rank=2)
+            check_gate(z, b, K, 8, score, groups=4, top=top, rank=1)
+        check_gate(z, b, 6, 8, score)
+
+
 # ------------------------------------------------------------------------------- gradient --
 
 def check_backward(z, idx, dg, score, renorm, scale, got):
