@@ -364,9 +364,10 @@ __global__ void __launch_bounds__(VPL <= 32 ? 256 : 128, gate_ctas(VPL))
         // bound on the error of a key k whose score is at most top
         auto error_of = [&](float k) {
             if (by_z) {
-                // logits are exact; where the 64-bit score hardly depends on them they decide nothing
-                if (sigmoid ? k < -700.0f : m0 - k > 700.0f) return __int_as_float(0x7f800000);
-                return 1e-13f + (sigmoid ? 1e-15f * __expf(fminf(k, 80.0f)) : 0.0f);
+                // logits are exact; where the 64-bit score hardly depends on them they decide nothing: next to
+                // 0, and sigmoids that are 1 in 64 bits (from 37 on, and by the line below up to 80)
+                if (sigmoid ? k < -700.0f || k > 80.0f : m0 - k > 700.0f) return __int_as_float(0x7f800000);
+                return 1e-13f + (sigmoid ? 1e-15f * __expf(k) : 0.0f);
             }
             const float rel = (sigmoid ? 0x1p-16f : 0x1p-15f) * (k - bmin), all = (sigmoid ? 7.0f : 33.0f * inv_S) * U23;
             return fminf(rel, all) + U23 * fabsf(k) + 1e-37f;
@@ -408,10 +409,17 @@ __global__ void __launch_bounds__(VPL <= 32 ? 256 : 128, gate_ctas(VPL))
                 rank += other > score || (other == score && q < lane);
             }
             kept = __ballot_sync(FULL, lane < o.groups && rank < o.top_groups);
-            // the groups that stay and those that leave are apart by their bounds (a score with an infinite key
-            // has no bound and is what it is in 64 bits)
-            const float low = redux_min(((kept >> lane) & 1u) ? score - err : __int_as_float(0x7f800000));
-            const float high = redux_max(lane < o.groups && !((kept >> lane) & 1u) ? score + err : NEG_INF);
+            // The groups that stay and those that leave are apart by their bounds. Where keys have a bias, an
+            // infinite score is what it is in 64 bits, and one of -inf that leaves is never above one that stays.
+            const bool sure = !by_z && isinf(score);
+            float low = __int_as_float(0x7f800000), high = NEG_INF;
+            if ((kept >> lane) & 1u) {
+                if (!sure) low = isinf(err) ? NEG_INF : score - err;
+            } else if (lane < o.groups && score != NEG_INF) {
+                high = score + err;
+            }
+            low = redux_min(low);
+            high = redux_max(high);
             if (!(low > high) || __any_sync(FULL, score != score)) {
                 keys64(zt, bias, E, sigmoid, m, row64);
                 kept = groups64(row64, o, size, team);

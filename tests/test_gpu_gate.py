@@ -252,6 +252,26 @@ def test_lowest_value_biases_beside_infinite_ones(cuda_device, score, low):
         check_gate(z, b, 6, 8, score)
 
 
+@pytest.mark.parametrize("K", [1, 2, 3])
+def test_sigmoid_logits_whose_scores_are_all_one(cuda_device, K):
+    """1 / (1 + e^-z) is 1 in 64 bits from z = 37 on: such logits tie, whatever they are."""
+    inf = math.inf
+    rng = np.random.default_rng(2)
+    z = torch.from_numpy(np.minimum(rng.standard_normal((6, 40)), 5.0).astype(np.float32)).cuda()
+    for row, at in enumerate(({3: 37.5, 20: inf}, {0: 37.5, 9: 1e25, 30: inf}, {7: 100.0, 8: 90.0, 9: 3e38, 39: inf},
+                              {1: inf, 2: 40.0}, {5: 79.0, 6: 81.0, 38: 2e20}, {i: 50.0 + i for i in range(40)})):
+        for i, v in at.items():
+            z[row, i] = v
+    for bf16 in (False, True):
+        v = z.bfloat16() if bf16 else z
+        for renorm in (True, False):
+            check_gate(v, None, K, 40, "sigmoid", renorm=renorm)
+            check_gate(v, torch.zeros(40, device="cuda"), K, 40, "sigmoid", renorm=renorm)
+            for groups, top in ((8, 1), (8, 3), (2, 1)):
+                check_gate(v, None, K, 40, "sigmoid", groups=groups, top=top, rank=1, renorm=renorm)
+                check_gate(v, None, K, 40, "sigmoid", groups=groups, top=top, rank=2, renorm=renorm)
+
+
 # ------------------------------------------------------------------------------- gradient --
 
 def check_backward(z, idx, dg, score, renorm, scale, got):
