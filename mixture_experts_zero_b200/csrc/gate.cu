@@ -507,7 +507,9 @@ __global__ void __launch_bounds__(VPL <= 32 ? 256 : 128, gate_ctas(VPL))
                     rank += kq > k || (kq == k && iq < i);
                 }
             }
-            // neighbours in the order: apart by their bounds, or equal in logit and bias
+            // The first K in the order: neighbours apart by their bounds, or equal in logit and bias. Every
+            // candidate behind them: the same against the K-th (neighbours that are apart say nothing about
+            // a third with a wider bound).
             __syncwarp();
             if (lane < total) cand[rank] = lane;
             __syncwarp();
@@ -515,13 +517,11 @@ __global__ void __launch_bounds__(VPL <= 32 ? 256 : 128, gate_ctas(VPL))
             const int i_s = __shfl_sync(FULL, i, from);
             const float k_s = __shfl_sync(FULL, k, from), e_s = __shfl_sync(FULL, err, from);
             const float z_s = __shfl_sync(FULL, z, from), b_s = __shfl_sync(FULL, b, from);
-            const float k_n = __shfl_down_sync(FULL, k_s, 1), e_n = __shfl_down_sync(FULL, e_s, 1);
-            const float z_n = __shfl_down_sync(FULL, z_s, 1), b_n = __shfl_down_sync(FULL, b_s, 1);
-            // Equal keys at the K-th place may have others behind them that fp32 cannot tell from them: the
-            // pairs that count reach to the end of that run.
+            const int other = lane < K - 1 ? lane + 1 : K - 1;
+            const float k_n = __shfl_sync(FULL, k_s, other), e_n = __shfl_sync(FULL, e_s, other);
+            const float z_n = __shfl_sync(FULL, z_s, other), b_n = __shfl_sync(FULL, b_s, other);
             const bool same = z_s == z_n && b_s == b_n;
-            const int last = K - 2 + __ffs(~(__ballot_sync(FULL, same) >> (K - 1)));
-            const bool close = lane <= last && lane + 1 < total && !(k_s - k_n > e_s + e_n) && !same;
+            const bool close = lane < total && !(fabsf(k_s - k_n) > e_s + e_n) && !same;
             my_idx = i_s;
             z = z_s;
             if (__any_sync(FULL, close)) {

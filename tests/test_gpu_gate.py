@@ -272,6 +272,26 @@ def test_sigmoid_logits_whose_scores_are_all_one(cuda_device, K):
                 check_gate(v, None, K, 40, "sigmoid", groups=groups, top=top, rank=2, renorm=renorm)
 
 
+@pytest.mark.parametrize("score", ["softmax", "sigmoid"])
+def test_an_uncertain_key_behind_two_certain_ones(cuda_device, score):
+    """The K-th and the key behind it are biases of experts without a score, which fp32 holds exactly and tells
+    apart; a third key, a score near e^-60 that fp32 holds within tens of steps, lies above both in 64 bits
+    and may lie below both in fp32."""
+    rng = np.random.default_rng(17)
+    zs = (-60.0 - 10.0 * rng.random(96)).astype(np.float32)
+    for z3 in zs:
+        # softmax: all of the rest is with expert 0, which is switched off
+        row = np.array([0.0 if score == "softmax" else -110.0, -110.0, -110.0, z3, -110.0, -110.0], np.float32)
+        s3 = R.scores(row[None], score)[0, 3]
+        for above in (6.0, 14.0):
+            b1 = np.float32(s3 * (1 - above * 2.0 ** -23))
+            b = [-math.inf, b1, b1 * np.float32(1 - 5 * 2.0 ** -23), 0.0, b1 * np.float32(0.5), -math.inf]
+            bt, zt = torch.tensor(b, dtype=torch.float32, device="cuda"), torch.from_numpy(row[None]).cuda()
+            for K in (1, 2):
+                idx, _ = B.lc_moe_gate(zt, bt, K, 6, score=score)
+                assert idx[0].cpu().tolist() == [3, 1][:K], (float(z3), above)
+
+
 # ------------------------------------------------------------------------------- gradient --
 
 def check_backward(z, idx, dg, score, renorm, scale, got):
