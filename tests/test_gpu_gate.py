@@ -394,6 +394,66 @@ def test_dense_gradient_of_a_row_that_is_nearly_one_hot(cuda_device, E, bf16):
     assert np.all(err <= tol), float((err / tol).max())
 
 
+def dense_gradient(z64, i, d):
+    """(dz, size) of softmax gates that are not renormalised, without a difference of nearly equal numbers:
+    s_e (sum over the picked experts u of s_u (ds_e - ds_u) + ds_e (sum of the other shares)) at the picks, where
+    ds_e is the sum of dgate over e's picks, and -s_i D elsewhere. size bounds the terms added; a sum over
+    several picks of an expert is rounded before it enters a difference, by as many half steps at most."""
+    T, E = z64.shape
+    s = R.scores(z64, "softmax")
+    want, size = np.zeros((T, E)), np.zeros((T, E))
+    for t in range(T):
+        picked = sorted(set(i[t].tolist()))
+        ds = np.array([d[t][i[t] == e].sum() for e in picked])
+        mag = np.array([np.abs(d[t][i[t] == e]).sum() for e in picked])
+        many = np.array([(i[t] == e).sum() for e in picked])
+        su = s[t, picked]
+        rest = np.delete(s[t], picked).sum()
+        want[t], size[t] = -s[t] * (su * ds).sum(), s[t] * (su * mag).sum()
+        diff = ds[:, None] - ds[None, :]
+        lost = R.U32 * ((many - 1) * mag)
+        want[t, picked] = su * ((su * diff).sum(1) + ds * rest)
+        size[t, picked] = su * ((su * np.abs(diff)).sum(1) + np.abs(ds) * rest) \
+            + su * (su * (lost[:, None] + lost[None, :])).sum(1) / R.U32
+    return want, size
+
+
+def check_dense(z, idx, dg, scale=1.0):
+    got = f64(B.lc_moe_gate_backward(z, idx, dg, renorm=False, scale=scale))
+    z64 = f64(z)
+    want, size = dense_gradient(z64, idx.cpu().numpy(), f64(dg))
+    want, size = scale * want, scale * size
+    tol = 2 * (3.4 * span(z64) + 100) * R.U32 * size + 1e-37
+    if z.dtype == torch.bfloat16:
+        tol = tol * (1 + R.U16) + R.U16 * np.abs(want)
+    err = np.abs(got - want)
+    assert np.all(err <= tol), float((err / tol).max())
+
+
+@pytest.mark.parametrize("bf16", [False, True])
+@pytest.mark.parametrize("E", [12, 77, 768, 2048])
+def test_dense_gradient_where_the_picks_hold_the_mass_together(cuda_device, E, bf16):
+    """Picks of comparable share with equal or nearly equal dgate: ds - D is what little the others hold."""
+    rng = np.random.default_rng(E)
+    for K in (2, 3, 5):
+        z = logits_of(8, E, E + K, False)
+        idx = np.stack([rng.permutation(E)[:K] for _ in range(8)]).astype(np.int32)
+        for t in range(8):
+            z[t, idx[t].tolist()] = torch.from_numpy((6.0 + 4 * t + rng.random(K)).astype(np.float32)).cuda()
+        z = z.bfloat16() if bf16 else z
+        it = torch.from_numpy(idx).cuda()
+        for dg in (np.ones((8, K)), 1 + 1e-6 * rng.standard_normal((8, K)), -3 + 0.1 * rng.random((8, K)),
+                   rng.standard_normal((8, K))):
+            dt = torch.from_numpy(dg.astype(np.float32)).cuda()
+            check_dense(z, it, dt)
+            check_dense(z, it, dt, scale=2.5)
+        # the first expert picked twice
+        rep = it.clone()
+        rep[:, -1] = rep[:, 0]
+        for dg in (np.full((8, K), 0.75), rng.standard_normal((8, K))):
+            check_dense(z, rep, torch.from_numpy(dg.astype(np.float32)).cuda())
+
+
 def test_gate_gradient_repeated_and_bad_picks(cuda_device):
     z = logits_of(4, 30, 3, False)
     idx = torch.tensor([[1, 1, 5, 1], [0, 29, 0, 29], [2, -1, 30, 4], [7, 8, 9, 10]], dtype=torch.int32, device="cuda")
