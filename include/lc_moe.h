@@ -382,8 +382,8 @@ int lc_moe_gate_backward(const lc_moe_shape* s, const lc_moe_gate_opts* o, const
  *   dx [T, d] bf16 = (sum of the gates of t's zero picks) dout_t: x's gradient through the zero
  *   experts alone
  * with fp32 products and sums. pair_row as lc_moe_permute makes it: a row is in one pick at most.
- * An entry >= y_rows sets LC_MOE_DEV_IDX_RANGE; its dgate is 0. dout, x, y are not written and must
- * not overlap dy and dx. ws: status only. */
+ * An entry >= y_rows sets LC_MOE_DEV_IDX_RANGE; its dgate is 0. dy, dgate and dx must not overlap each
+ * other or an input (else LC_MOE_ERR_INVALID_ARG). ws: status only. */
 int lc_moe_combine_backward(const lc_moe_shape* s, const void* dout, const void* x, const void* y, int64_t y_rows,
                             const float* gate, const int32_t* pair_row, void* dy, float* dgate, void* dx, void* ws,
                             size_t ws_bytes, void* stream);

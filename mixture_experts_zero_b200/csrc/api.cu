@@ -4,6 +4,7 @@
 // launch sequence of the layer on the caller's stream. The library allocates nothing; the only
 // synchronising call is lc_moe_read_status.
 #include <atomic>
+#include <initializer_list>
 #include <mutex>
 
 #include "common.cuh"
@@ -21,6 +22,26 @@ constexpr size_t kStatusBytes = 256;
 size_t align_up(size_t v) { return (v + kAlign - 1) / kAlign * kAlign; }
 
 bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
+
+// Whether two buffers share a byte (an empty one shares none).
+struct Span {
+    const void* p;
+    int64_t bytes;
+};
+bool overlap(const Span& a, const Span& b) {
+    const uintptr_t p = reinterpret_cast<uintptr_t>(a.p), q = reinterpret_cast<uintptr_t>(b.p);
+    return a.bytes > 0 && b.bytes > 0 && (p <= q ? q - p < static_cast<uint64_t>(a.bytes) : p - q < static_cast<uint64_t>(b.bytes));
+}
+// Whether one of the written buffers shares a byte with a read one or with another written one.
+bool overlap(std::initializer_list<Span> written, std::initializer_list<Span> read) {
+    for (const Span* w = written.begin(); w != written.end(); ++w) {
+        for (const Span* v = written.begin(); v != w; ++v)
+            if (overlap(*w, *v)) return true;
+        for (const Span& r : read)
+            if (overlap(*w, r)) return true;
+    }
+    return false;
+}
 
 int check_shape(const lc_moe_shape* s) {
     if (!s) return LC_MOE_ERR_INVALID_ARG;
@@ -577,7 +598,11 @@ int lc_moe_combine_backward(const lc_moe_shape* s, const void* dout, const void*
     for (const void* p : {dout, x, y, static_cast<const void*>(dy), static_cast<const void*>(dx),
                           static_cast<const void*>(ws)})
         if (p && !aligned16(p)) return LC_MOE_ERR_MISALIGNED;
-    if ((y && dy == y) || dx == x || dx == dout) return LC_MOE_ERR_INVALID_ARG;  // not in place
+    const int64_t row = static_cast<int64_t>(s->d) * 2, picks = static_cast<int64_t>(s->T) * s->K * 4;
+    const int64_t y_bytes = (y_rows < INT32_MAX ? y_rows : INT32_MAX) * row;  // pair_row reaches no further
+    if (overlap({{dy, y_bytes}, {dx, s->T * row}, {dgate, picks}},
+                {{dout, s->T * row}, {x, s->T * row}, {y, y_bytes}, {gate, picks}, {pair_row, picks}}))
+        return LC_MOE_ERR_INVALID_ARG;
     LC_TRY(device_ok());
     LC_CUDA(launch_combine_backward(dout, x, y, y_rows, gate, pair_row, s->T, s->d, s->K, dy, dgate, dx,
                                     at<uint32_t>(ws, 0), static_cast<cudaStream_t>(stream)));

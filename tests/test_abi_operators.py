@@ -218,3 +218,41 @@ def test_options_beyond_32_bits_are_refused(at):
         a[at] = v
         with pytest.raises(B.LcMoeError, match="invalid argument"):
             B._gate_opts("softmax", *a, True, 1.0)
+
+
+def _at(v):
+    return ctypes.c_void_p(v)
+
+
+# one token row of d = 128 is 256 bytes, T = 16 rows 4096; K = 3
+ROOM = dict(dout=1 << 16, x=2 << 16, y=3 << 16, g=4 << 16, pr=5 << 16, dy=6 << 16, dg=7 << 16, dx=8 << 16)
+
+
+@pytest.mark.parametrize("out,rows", [("dy", 48), ("dx", 16)])
+@pytest.mark.parametrize("other", ["dout", "x", "y", "dy", "dx", "g", "pr", "dg"])
+def test_combine_backward_refuses_buffers_that_overlap(lib, out, rows, other):
+    """Whatever a pick reads, another pick's write must not reach: one buffer for two, or parts of one."""
+    if out == other:
+        return
+    size = dict(dout=4096, x=4096, y=48 * 256, dy=48 * 256, dx=4096, g=192, pr=192, dg=192)
+    for delta in (0, size[other] // 16 * 16 - 16, 16 - rows * 256):
+        a = {k: _at(v) for k, v in ROOM.items()}
+        a[out] = _at(ROOM[other] + delta)
+        assert lib.lc_moe_combine_backward(shape(), a["dout"], a["x"], a["y"], 48, a["g"], a["pr"], a["dy"], a["dg"], a["dx"],
+                                           P, 256, None) == INV, delta
+    # next to it
+    for at in (ROOM[other] + size[other], ROOM[other] - rows * 256):
+        a = {k: _at(v) for k, v in ROOM.items()}
+        a[out] = _at(at)
+        if not torch.cuda.is_available():
+            assert lib.lc_moe_combine_backward(shape(), a["dout"], a["x"], a["y"], 48, a["g"], a["pr"], a["dy"], a["dg"],
+                                               a["dx"], P, 256, None) == B.ERR_CUDA
+
+
+def test_combine_backward_refuses_dgate_over_the_gates(lib):
+    """The gates of a token are read by every block that has some of its picks."""
+    a = {k: _at(v) for k, v in ROOM.items()}
+    for other in ("g", "pr"):
+        for delta in (0, 188, -188):
+            assert lib.lc_moe_combine_backward(shape(), a["dout"], a["x"], a["y"], 48, a["g"], a["pr"], a["dy"],
+                                               _at(ROOM[other] + delta), a["dx"], P, 256, None) == INV
