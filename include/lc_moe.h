@@ -367,9 +367,9 @@ int lc_moe_gate(const lc_moe_shape* s, const lc_moe_gate_opts* o, const void* lo
                 const float* bias, int32_t* idx, float* gate, int32_t* counts, void* ws, size_t ws_bytes,
                 void* stream);
 
-/* Gradient of the gates for the logits, the picks held fixed: dlogits [T, E] (the logits' type; not
- * the logits' own buffer) from logits, idx [T, K] and dgate [T, K] fp32. Of the options score,
- * renorm and scale count. An entry of idx outside [0, E) sets LC_MOE_DEV_IDX_RANGE and counts as
+/* Gradient of the gates for the logits, the picks held fixed: dlogits [T, E] (the logits' type;
+ * must not overlap an input, else LC_MOE_ERR_INVALID_ARG) from logits, idx [T, K] and dgate [T, K] fp32.
+ * Of the options score, renorm and scale count. An entry of idx outside [0, E) sets LC_MOE_DEV_IDX_RANGE and counts as
  * no pick; an expert picked twice gets the sum. The bias has no gradient. ws: status only. */
 int lc_moe_gate_backward(const lc_moe_shape* s, const lc_moe_gate_opts* o, const void* logits,
                          int32_t logits_type, const int32_t* idx, const float* dgate, void* dlogits, void* ws,

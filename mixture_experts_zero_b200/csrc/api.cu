@@ -581,6 +581,8 @@ int lc_moe_gate_backward(const lc_moe_shape* s, const lc_moe_gate_opts* o, const
     const uintptr_t unit = logits_type == LC_MOE_BF16 ? 2 : 4;
     if (reinterpret_cast<uintptr_t>(logits) % unit || reinterpret_cast<uintptr_t>(dlogits) % unit || !aligned16(ws))
         return LC_MOE_ERR_MISALIGNED;
+    const int64_t row = static_cast<int64_t>(s->N + s->Z) * unit, picks = static_cast<int64_t>(s->T) * s->K * 4;
+    if (overlap({{dlogits, s->T * row}}, {{logits, s->T * row}, {idx, picks}, {dgate, picks}})) return LC_MOE_ERR_INVALID_ARG;
     LC_TRY(device_ok());
     LC_CUDA(launch_gate_backward(logits, logits_type == LC_MOE_BF16, idx, dgate, s->T, s->N + s->Z, s->K, *o, dlogits,
                                  at<uint32_t>(ws, 0), static_cast<cudaStream_t>(stream)));

@@ -256,3 +256,14 @@ def test_combine_backward_refuses_dgate_over_the_gates(lib):
         for delta in (0, 188, -188):
             assert lib.lc_moe_combine_backward(shape(), a["dout"], a["x"], a["y"], 48, a["g"], a["pr"], a["dy"],
                                                _at(ROOM[other] + delta), a["dx"], P, 256, None) == INV
+
+
+@pytest.mark.parametrize("kind,width", [(0, 4), (1, 2)])
+def test_gate_backward_refuses_buffers_that_overlap(lib, kind, width):
+    """dlogits [16, 12] over a part of the logits, of idx or of dgate."""
+    n, z, i, g = 16 * 12 * width, 1 << 16, 2 << 16, 3 << 16
+    for at in (z, z + n - width, z - n + width, i + 188, i - n + 4, g + 188, g - n + 4):
+        assert lib.lc_moe_gate_backward(shape(), None, _at(z), kind, _at(i), _at(g), _at(at), P, 256, None) == INV
+    if not torch.cuda.is_available():
+        for at in (z + n, z - n, i + 192, g - n):
+            assert lib.lc_moe_gate_backward(shape(), None, _at(z), kind, _at(i), _at(g), _at(at), P, 256, None) == B.ERR_CUDA
