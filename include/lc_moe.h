@@ -414,7 +414,8 @@ int lc_moe_quantize_w4(const void* src, int64_t rows, int32_t cols, int32_t grou
  * w2q [N, d, I/2] with w2_scale [N, d/16, I/group, 16]. h and y as there (bf16 at both); rows
  * >= offsets[N] are not written. An expert whose rows are not within [0, T*K], or begin before the end
  * of the last expert that was not skipped, sets LC_MOE_DEV_IDX_RANGE and is skipped: its rows are not
- * written. ws: status only. */
+ * written. h must not overlap x_perm, y or offsets, nor y offsets (else LC_MOE_ERR_INVALID_ARG); y may
+ * lie over x_perm. ws: status only. */
 int lc_moe_expert_ffn_w4(const lc_moe_shape* s, const void* x_perm, const int32_t* offsets, const void* w13q,
                          const void* w13_scale, const void* w2q, const void* w2_scale, int32_t group, void* h,
                          void* y, void* ws, size_t ws_bytes, void* stream);

@@ -636,9 +636,13 @@ int lc_moe_expert_ffn_w4(const lc_moe_shape* s, const void* x_perm, const int32_
     for (const void* p : {x_perm, w13q, w13_scale, w2q, w2_scale, static_cast<const void*>(h),
                           static_cast<const void*>(y), static_cast<const void*>(ws)})
         if (!aligned16(p)) return LC_MOE_ERR_MISALIGNED;
+    const int64_t rows_cap = static_cast<int64_t>(s->T) * s->K;
+    // h is complete before y begins: y may lie over x_perm
+    const Span offs{offsets, (static_cast<int64_t>(s->N) + 1) * 4}, y_span{y, rows_cap * s->d * 2};
+    if (overlap({{h, rows_cap * s->I * 2}}, {{x_perm, rows_cap * s->d * 2}, y_span, offs}) || overlap(y_span, offs))
+        return LC_MOE_ERR_INVALID_ARG;
     LC_TRY(device_ok());
     cudaStream_t st = static_cast<cudaStream_t>(stream);
-    const int64_t rows_cap = static_cast<int64_t>(s->T) * s->K;
     uint32_t* status = at<uint32_t>(ws, 0);
     LC_CUDA(launch_swiglu_w4(x_perm, rows_cap, offsets, s->N, w13q, w13_scale, group, s->d, s->I, h, status, st));
     LC_CUDA(launch_down_w4(h, rows_cap, offsets, s->N, w2q, w2_scale, group, s->d, s->I, y, status, st));

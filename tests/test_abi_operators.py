@@ -267,3 +267,18 @@ def test_gate_backward_refuses_buffers_that_overlap(lib, kind, width):
     if not torch.cuda.is_available():
         for at in (z + n, z - n, i + 192, g - n):
             assert lib.lc_moe_gate_backward(shape(), None, _at(z), kind, _at(i), _at(g), _at(at), P, 256, None) == B.ERR_CUDA
+
+
+def test_w4_ffn_refuses_h_over_its_inputs(lib):
+    """H [48, 64] is written while rows of x_perm [48, 128] are read, and read while Y [48, 128] is written."""
+    x, h, y, off = 1 << 20, 2 << 20, 3 << 20, 4 << 20
+
+    def call(h, y):
+        return lib.lc_moe_expert_ffn_w4(shape(), _at(x), _at(off), P, P, P, P, 32, _at(h), _at(y), P, 256, None)
+    for at in (x, x + 48 * 256 - 16, x - 48 * 128 + 16, y, y + 48 * 256 - 16, y - 48 * 128 + 16, off, off + 16):
+        assert call(at, y) == INV
+    assert call(h, off - 48 * 256 + 16) == INV
+    if not torch.cuda.is_available():
+        for at in (x + 48 * 256, y - 48 * 128):
+            assert call(at, y) == B.ERR_CUDA
+        assert call(h, x) == B.ERR_CUDA     # Y over x_perm: H is complete before Y begins

@@ -211,6 +211,20 @@ def test_bad_offsets_are_reported_and_skipped(cuda_device):
         assert B.lc_moe_read_status(ws, raise_on_error=False) == B.DEV_IDX_RANGE
 
 
+def test_y_over_its_rows(cuda_device):
+    """H is complete before Y begins, so Y may take the place of x_perm; rows of no expert stay."""
+    N, d, I, group, counts = 4, 512, 1024, 64, [3, 40, 0, 17]
+    _, _, q = weights(N, d, I, group, 18)
+    x = torch.randn(sum(counts) + 4, d, device="cuda").bfloat16()
+    off = torch.tensor(np.concatenate([[0], np.cumsum(counts)]), dtype=torch.int32, device="cuda")
+    h, y = B.lc_moe_expert_ffn_w4(x, off, *q, 64, 1)
+    for _ in range(5):
+        over = x.clone()
+        h2, y2 = B.lc_moe_expert_ffn_w4(over, off, *q, 64, 1, y=over)
+        assert y2 is over and torch.equal(h[:60], h2[:60]) and torch.equal(y[:60], over[:60])
+        assert torch.equal(over[60:], x[60:])
+
+
 @pytest.mark.parametrize("rows,offsets,taken", [
     (8, [0, 3, 2, 8], [0]),            # expert 2 begins inside expert 0
     (8, [0, 3, 6, 9], [0, 1]),
