@@ -218,6 +218,10 @@ struct Int {
 constexpr int W4_CTAS = 2;  // to an SM
 // ring, partial sums, prefix sums and numbers of the live experts
 constexpr size_t w4_smem(int n) { return RING_BYTES + RED_BYTES + (n + 1) * 4 + n * 2; }
+// CTAs that an SM's 228 KB hold (1 KB of it goes to each): 2 up to 1194 experts, 1 above. The tables are
+// not cut to the rows of the call: offsets that are out of order may name more experts than it has rows.
+constexpr int w4_ctas(int n) { return W4_CTAS * (w4_smem(n) + 1024) <= 228 * 1024 ? W4_CTAS : 1; }
+static_assert(w4_ctas(1194) == 2 && w4_ctas(1195) == 1 && w4_smem(2048) <= 227 * 1024, "shared memory");
 
 // Item: `8 / split` tiles of 64 HALVES weight rows of one expert (as many gate as up rows, or output
 // features) times up to 8 MAXNT of its rows. The CTA's warps form 8 / split teams, one for each
@@ -569,7 +573,7 @@ cudaError_t launch_w4_t(const W4Args& a, cudaStream_t st) {
     attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attr.val.programmaticStreamSerializationAllowed = 1;
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(di->sm_count * W4_CTAS);
+    cfg.gridDim = dim3(di->sm_count * w4_ctas(a.N));  // one wave
     cfg.blockDim = dim3(W4_THREADS);
     cfg.dynamicSmemBytes = smem;
     cfg.stream = st;
@@ -583,12 +587,12 @@ cudaError_t launch_w4_t(const W4Args& a, cudaStream_t st) {
 // Warps on a tile's reduction. Fewer warps mean fewer sums to join, but also fewer and longer items:
 // a split that leaves a warp 16 steps of 64 columns, raised while there are fewer than 8 items an SM
 // (one token over 8 experts, down product: 22 us with 4 warps on a tile, 20 with 8).
-int split_of(const W4Args& a, int tile_rows, int tok) {
+int split_of(const W4Args& a, int tile_rows, int tok, int sm_count) {
     const int64_t tiles = a.m / tile_rows, row_tiles = (a.rows_cap < a.N ? a.rows_cap : a.N) + a.rows_cap / tok;
     const int steps = a.k / 64;
     int split = 1;
     while (split < W4_WARPS && split * 2 <= steps &&
-           (steps / split >= 32 || row_tiles * ((tiles * split + W4_WARPS - 1) / W4_WARPS) < 8 * 148))
+           (steps / split >= 32 || row_tiles * ((tiles * split + W4_WARPS - 1) / W4_WARPS) < 8 * sm_count))
         split *= 2;
     return split;
 }
@@ -598,7 +602,9 @@ cudaError_t launch_w4_n(W4Args a, cudaStream_t st) {
     a.code_blk = static_cast<int64_t>(a.k / 64) * 512;
     a.scale_blk = static_cast<int64_t>(a.k / a.group) * 32;
     a.code_up = SWIGLU ? a.m / 32 * a.code_blk : 2 * a.code_blk;
-    a.split = split_of(a, 64 * HALVES, 8 * MAXNT);
+    const DevInfo* di = current_device_info();
+    if (!di) return cudaErrorUnknown;
+    a.split = split_of(a, 64 * HALVES, 8 * MAXNT, di->sm_count);
     return a.group == 32 ? launch_w4_t<SWIGLU, true, HALVES, MAXNT>(a, st) : launch_w4_t<SWIGLU, false, HALVES, MAXNT>(a, st);
 }
 
