@@ -28,6 +28,8 @@
 // token in 5 us. The choice by K rounds over all keys in 64 bits took 457 and 412 us.
 #include <cuda_bf16.h>
 
+#include <type_traits>
+
 #include "common.cuh"
 
 namespace lcmoe {
@@ -608,9 +610,11 @@ struct Vec<__nv_bfloat16, 8> {
 // One warp per token. The row is written in full first, then the chosen entries over it. V: values
 // a lane holds of the row (0: nothing of it is needed, every entry that is not chosen is 0). Rows
 // are read and written once, in 16-byte pieces (W values) where E and the pointers allow; what
-// bounds it is memory: 16384 x 768 fp32 in 20.4 us (5.0 TB/s) with inputs that are not in L2.
+// bounds it is memory: 16384 x 768 fp32 in 20.4 us (5.0 TB/s) with inputs that are not in L2. Up to 24
+// values a lane 40 registers hold them (the sums over the picks spill 5, on their branch alone): 6 CTAs an
+// SM take 21.3 us where 64 registers and 4 CTAs take 21.6 (six sets of tensors in turn).
 template <class LT, int W, int V>
-__global__ void __launch_bounds__(GATE_THREADS)
+__global__ void __launch_bounds__(GATE_THREADS, V <= 24 ? 6 : 1)
     gate_backward_kernel(const LT* __restrict__ logits, const int32_t* __restrict__ idx,
                          const float* __restrict__ dgate, int T, int E, int K, lc_moe_gate_opts o,
                          LT* __restrict__ dlogits, uint32_t* __restrict__ status) {
@@ -696,19 +700,20 @@ __global__ void __launch_bounds__(GATE_THREADS)
             // does their part ds * rest, and ds - D keeps within some tens of half steps of the sizes added
             // (from 0.5 on 16.0 us from L2 at 16384 x 768, from 0.75 on 14.8, from 0.9 on 14.4).
             const uint32_t firsts = __ballot_sync(FULL, first);
-            unsigned long long chosen = 0;  // bits of this lane's places
+            using Bits = typename std::conditional<(V > 32), unsigned long long, uint32_t>::type;
+            Bits chosen = 0;  // of this lane's places
             float apart = 0.0f;
             for (int q = 0; q < K; ++q) {
                 const int iq = __shfl_sync(FULL, i, q);
                 const float s_q = __shfl_sync(FULL, share, q), apart_q = ds - __shfl_sync(FULL, ds, q);
                 if (!((firsts >> q) & 1u)) continue;  // no pick, or an expert that an earlier pick has named
                 const int place = iq / W;
-                if (place % 32 == lane) chosen |= 1ull << (place / 32 * W + iq % W);
+                if (place % 32 == lane) chosen |= Bits(1) << (place / 32 * W + iq % W);
                 apart = fmaf(s_q, apart_q, apart);
             }
             float rest = 0.0f;
 #pragma unroll
-            for (int j = 0; j < V; ++j) rest += (chosen >> j) & 1ull ? 0.0f : e[j];
+            for (int j = 0; j < V; ++j) rest += (chosen >> j) & 1u ? 0.0f : e[j];
             total = share * fmaf(ds, warp_sum(rest) * inv_S, apart);
         } else {
             total = share * (ds - D);
