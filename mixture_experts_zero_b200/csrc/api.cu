@@ -145,7 +145,7 @@ int check_gate(const lc_moe_shape* s, const lc_moe_gate_opts* o) {
     return LC_MOE_OK;
 }
 
-// Group of the 4-bit weights for a checked shape (0: not 4-bit weights).
+// Columns to a scale of the 4-bit weights, for a checked shape.
 int check_group(const lc_moe_shape* s, int32_t group) {
     if (group != 32 && group != 64 && group != 128) return LC_MOE_ERR_INVALID_ARG;
     return s->d % group || s->I % group ? LC_MOE_ERR_UNSUPPORTED_SHAPE : LC_MOE_OK;

@@ -18,14 +18,18 @@
 // The picks are integers, so they are decided in 64 bits: two programs that evaluate the formula
 // in 64 bits agree on them unless two keys lie within about 1e-16 of each other. The kernel gets
 // there from fp32 keys with a bound on their error: it collects the keys within the bounds of the
-// K-th largest, sorts them, and evaluates them again in 64 bits where two neighbours in that order
-// are not apart by their bounds (a few tokens in a thousand).
+// K-th largest, sorts them, and evaluates them again in 64 bits where two neighbours among the first K
+// or the K-th and one behind it are not apart by their bounds (a few tokens in a thousand). More than
+// 32 candidates, or fewer than K lanes with a key of the groups that stay, send the token to K rounds
+// over all its keys in 64 bits.
 //
 // One warp per token, E / 32 logits a lane, each read once. What bounds it is instructions and their
 // latency: per logit a load, an exponential, a key and three comparisons, then some hundreds a token
 // for the choice (about 1050 in all at E = 768). Measured on a B200 with inputs that are not in L2:
-// 16384 x 768 softmax with a bias, K = 12, in 37 us (1.4 TB/s); with 8 groups of sigmoid scores 51 us; one
-// token in 5 us. The choice by K rounds over all keys in 64 bits took 457 and 412 us.
+// 16384 x 768 softmax with a bias, K = 12, in 39 us (1.3 TB/s), with 8 groups of sigmoid scores 53 us; from L2
+// 33 and 49 us; one token in 5 us. Rows of equal logits take the K rounds: a batch of nothing else 198 and
+// 243 us from L2, one with a quarter of them 151 and 197, with one in a hundred 60 and 82. 128 experts in 16
+// groups of which 2 stay share lanes, so that a token in five takes them: 42 us, without groups 18.
 #include <cuda_bf16.h>
 
 #include <type_traits>
@@ -269,8 +273,9 @@ constexpr float U23 = 1.1920929e-07f;
 // team: lanes to a group when group scores are taken (a power of two, so that all groups run at once);
 // a group's keys start size + pad words apart in the warp's row of row_len doubles, so that the
 // teams' reads fall on different banks.
-// CTAs to an SM: 64 registers a thread hold up to 12 keys a lane without spills, more keys want 128
-// (16384 x 768: 33.3 us with 2 CTAs, 33.7 with 3, 34.2 with 4).
+// CTAs to an SM: 64 registers a thread hold up to 12 keys a lane without spills, up to 32 keys want 128
+// (16384 x 768 from L2: 32.9 us with 2 CTAs, 34.8 with 3, 35.0 with 4). 64 keys a lane take blocks of 128
+// threads, which 2 CTAs leave up to 255 registers each.
 constexpr int gate_ctas(int vpl) { return vpl <= 12 ? 4 : 2; }
 
 // FILLED: E is 32 VPL.
@@ -363,7 +368,7 @@ __global__ void __launch_bounds__(VPL <= 32 ? 256 : 128, gate_ctas(VPL))
                 for (int j = 0; j < VPL; ++j) v[j] = fmaf(v[j], inv_S, in(j) ? 0.0f : NEG_INF);
             }
         }
-        // bound on the error of a key k whose score is at most top
+        // bound on the error of a key k, whose score is at most k - bmin
         auto error_of = [&](float k) {
             if (by_z) {
                 // logits are exact; where the 64-bit score hardly depends on them they decide nothing: next to

@@ -27,14 +27,16 @@
 // weight.
 //
 // Measured on a B200 (copy rate 6.5 TB/s): 32 tokens over 115 experts of 6144 x 2048, group 64, 2.3 GB
-// in 455 us (5.1 TB/s); 128 tokens over 512 experts, 9.0 GB in 1.95 ms; one token over 8 experts, 156 MB
-// in 47 us. It is bound by instructions: 7 integer operations for 8 weights on a half-rate pipe, and
-// the mma.sync next to them (the stream without the products takes 345 us, without unpacking 374).
+// in 450 us (5.1 TB/s); 128 tokens over 512 experts, 9.0 GB in 1.69 ms at 1965 MHz and, call after call, in
+// 1.95 ms at the 1.70 GHz that the 1000 W limit leaves; one token over 8 experts, 156 MB in 47 us. The
+// time goes with the SM clock, not with HBM. 7 integer operations for 8 weights on a half-rate pipe and
+// the mma.sync next to them make up most of it (the stream without the products takes 345 us, without
+// unpacking 374; these instructions alone would take three quarters of the cycles).
 // No gain came from byte permutes or multiplications in place of shifts, from more logic operations
 // for fewer shifts, from products of 16 + n or 128 + n that start at -24 or -136 times the sum of the
 // activations (which drops the subtraction), from ring stages of one block by 256 columns, or from
-// 24 warps an SM. With many rows an expert it
-// reaches 0.13 to 0.21 PFLOP/s.
+// 24 warps an SM. With many rows an expert it reaches 0.13 to 0.22 PFLOP/s: the weights are unpacked
+// again for every 16 of them.
 #include "common.cuh"
 
 namespace lcmoe {
@@ -71,7 +73,8 @@ __device__ __forceinline__ float silu_mul(float g, float u) { return __fdividef(
 
 // One warp per 16 rows x (64 columns, or 128 when the group is 128). scale = bf16(amax / 7) (1 for
 // a group whose scale would be 0), code = 8 + round(w / scale), a division in fp32, to nearest
-// even, within -7..7.
+// even, within -7..7. Run once for a model's weights: 64 matrices of 4096 x 6144 in 1.96 to 2.29 ms (2.07 to
+// 1.79 TB/s, groups of 128 to 32), bound by the pipe of reciprocals, roundings and conversions (73 to 76 %).
 __global__ void __launch_bounds__(256)
     quantize_w4_kernel(const __nv_bfloat16* __restrict__ src, int64_t tile_rows, int cols, int group,
                        uint4* __restrict__ codes, uint32_t* __restrict__ scale) {

@@ -252,6 +252,7 @@ def test_lowest_value_biases_beside_infinite_ones(cuda_device, score, low):
         check_gate(z, b, 6, 8, score)
 
 
+@pytest.mark.filterwarnings("ignore::RuntimeWarning")  # infinities in the plain form
 @pytest.mark.parametrize("K", [1, 2, 3])
 def test_sigmoid_logits_whose_scores_are_all_one(cuda_device, K):
     """1 / (1 + e^-z) is 1 in 64 bits from z = 37 on: such logits tie, whatever they are."""
