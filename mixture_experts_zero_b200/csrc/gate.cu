@@ -616,8 +616,8 @@ struct Vec<__nv_bfloat16, 8> {
 // a lane holds of the row (0: nothing of it is needed, every entry that is not chosen is 0). Rows
 // are read and written once, in 16-byte pieces (W values) where E and the pointers allow; what
 // bounds it is memory: 16384 x 768 fp32 in 20.4 us (5.0 TB/s) with inputs that are not in L2. Up to 24
-// values a lane 40 registers hold them (the sums over the picks spill 5, on their branch alone): 6 CTAs an
-// SM take 21.3 us where 64 registers and 4 CTAs take 21.6 (six sets of tensors in turn).
+// values a lane 40 registers do with 20 bytes of spills: 6 CTAs an SM take 21.3 us where 64 registers and 4
+// CTAs take 21.6 (six sets of tensors in turn).
 template <class LT, int W, int V>
 __global__ void __launch_bounds__(GATE_THREADS, V <= 24 ? 6 : 1)
     gate_backward_kernel(const LT* __restrict__ logits, const int32_t* __restrict__ idx,
